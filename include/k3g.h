@@ -456,6 +456,86 @@ int k3g_cache_decode_step(k3g_cache *c, float *y, const float *x, const int32_t 
  * resident) and the request histogram (uint64 [n_total]). */
 int k3g_cache_query(const k3g_cache *c, k3g_cache_stats *stats, int32_t *slot_of, uint64_t *hist);
 
+/* ---- microscaled activations: quantiser, norm, and products with MXFP4 weights --- */
+
+/* Element types of the dense tensors these calls take or write. */
+typedef enum { K3G_F32 = 0, K3G_BF16 = 1, K3G_F16 = 2 } k3g_type;
+
+/* Microscaled row formats: every 32 entries of a row share one ue8m0 scale
+ * byte s, an entry is code * 2^(s-127), and a group whose byte is 255
+ * contributes nothing (as in the weights).
+ *   K3G_MXFP4: e2m1 codes, two per byte, codes [rows][in/2], the weights' layout;
+ *   K3G_MXFP8: e4m3 codes (largest 448, no infinity), codes [rows][in]. */
+typedef enum { K3G_MXFP4 = 0, K3G_MXFP8 = 1 } k3g_mx_format;
+
+/* A microscaled matrix of `rows` rows of `in` entries: codes 16-byte aligned,
+ * scales [rows][in/32], both contiguous. in a positive multiple of 32, at most
+ * 65536 (K3G_EUNSUPPORTED beyond); rows >= 0 (rows = 0: the call enqueues
+ * nothing and the pointers may be null). */
+typedef struct {
+    uint8_t *codes, *scales;
+    int32_t rows, in, format;
+} k3g_mx;
+
+/* x [rows][in] (type x_type, rows x_stride >= in entries apart) -> q. Per
+ * 32-group: 2^e is the smallest power of two, e >= -126, with max|x| <= M 2^e
+ * (M = 6 for MXFP4, 448 for MXFP8), so nothing is cut off; the byte is e + 127
+ * (1 for a group of zeros) and each code is x / 2^e rounded to nearest, ties to
+ * the even code. A group that holds a NaN or an infinity has no value in
+ * these formats: its byte is 255 and its codes are 0, so it contributes
+ * nothing. x aligned to its entries. q must not overlap x. */
+int k3g_mx_quantize(const k3g_mx *q, const void *x, int x_type, int64_t x_stride, void *stream);
+
+/* q -> y [rows][in] (rows y_stride entries apart): code * 2^(s-127) rounded
+ * once to y_type (to nearest even; beyond its range: infinity), 0 for a group
+ * whose byte is 255. y must not overlap q. */
+int k3g_mx_dequantize(void *y, int y_type, int64_t y_stride, const k3g_mx *q, void *stream);
+
+/* The residual's addition and the RMS norm of each of n_rows rows of `in`
+ * entries: s = x + r in fp32 (s = x where r is null), n = s / sqrt(mean(s^2) +
+ * eps) * gamma, the mean and n in fp32 from the unrounded s. Written where the
+ * pointer is not null: sum = s and y = n, each rounded once to `type`, and
+ * q = n quantised as k3g_mx_quantize does from the unrounded n (q->rows =
+ * n_rows, q->in = in). At least one of y and q. x, r, sum and y are of `type`,
+ * rows x_stride, r_stride, sum_stride, y_stride entries apart (each >= in);
+ * gamma fp32 [in]; eps >= 0. sum or y may be x or r itself (same pointer and
+ * stride); any other overlap of an output is K3G_EINVAL. in as k3g_mx. */
+int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, const k3g_mx *q,
+                    const void *x, int64_t x_stride, const void *r, int64_t r_stride, int type,
+                    const float *gamma, float eps, int n_rows, int in, void *stream);
+
+/* y[t][n] = sum over 32-groups of 2^(sa-127) 2^(sw-127) sum_j a_tj w_nj for a
+ * microscaled a [T][in] and an MXFP4 w [rows][in]: the block-scaled matrix
+ * cores on both as they are stored, products exact, sums in fp32, rounded once
+ * to y_type. y rows y_stride >= w->rows entries apart. A group with byte 255 in
+ * a or in w adds nothing (e4m3 NaN codes, which the quantiser does not
+ * write, propagate wherever a's byte is not 255). y must overlap no input. */
+int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_mxfp4 *w, void *stream);
+
+/* A bank's tensors as a grouped product names them. */
+typedef enum { K3G_W1 = 0, K3G_W3 = 1, K3G_W2 = 2 } k3g_bank_tensor;
+
+/* The same product grouped by expert over ragged groups: rows offsets[e] ..
+ * offsets[e+1]-1 of y (device int32 [n_experts+1], as the bucket writes them)
+ * are expert e's, y[p] = W_e a[src(p)], where W is the named tensor of the
+ * bank and src(p) = p, or perm[p] / top_k where perm is given (device int32
+ * [n_rows], the bucket's sorted position -> pair id t*top_k+k). Groups may be
+ * empty; rows below offsets[0] or from offsets[n_experts] on are left as they
+ * were. Preconditions (not checked on the device, but nothing out of range is
+ * read or written without them): offsets ascending within [0, n_rows], perm
+ * values in [0, a->rows * top_k). Without perm a->rows >= n_rows. y has n_rows
+ * rows. n_experts <= 2048; with perm a->rows * in < 2^31. */
+int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_expert_bank *bank,
+                          int tensor, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows,
+                          void *stream);
+
+/* The experts' gated up-products, grouped the same way: h[p] = SiTU(w1 a, w3 a)
+ * of p's expert for a = a[src(p)], in fp32 and then quantised as
+ * k3g_mx_quantize does (h->in = bank->inter, h->rows >= n_rows; formats of a and
+ * h are independent). h must overlap no input. */
+int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *bank, const int32_t *offsets,
+                       const int32_t *perm, int top_k, int n_rows, void *stream);
+
 /* ---- stage hooks used by the bit-exact checks ----------------------------- */
 
 /* Per row and 32-group: s = max|x|/127 (fp32), q = rint(x/s) clamped to

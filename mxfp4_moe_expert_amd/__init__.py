@@ -8,7 +8,9 @@ fallback of any kind. PyTorch provides device memory and streams.
 
 The names match the C entry points: k3g_mxfp4_gemv, k3g_expert_glu,
 k3g_moe_route, k3g_moe_layer, k3g_latent_moe_block, k3g_quantize_i8_groups,
-k3g_mxfp4_idot_groupsums.
+k3g_mxfp4_idot_groupsums, and for microscaled activations k3g_mx_quantize,
+k3g_mx_dequantize, k3g_add_rmsnorm, k3g_mx_matmul, k3g_mx_grouped_matmul,
+k3g_mx_grouped_glu.
 """
 
 from __future__ import annotations
@@ -33,6 +35,9 @@ OP_MOE_ROUTE = 2
 OP_MOE_LAYER = 3
 OP_LATENT_BLOCK = 4
 GROUP = 32
+MXFP4, MXFP8 = 0, 1  # microscaled row formats: e2m1 (two a byte) and e4m3 codes, a ue8m0 scale per 32 entries
+W1, W3, W2 = 0, 1, 2  # a bank's tensors as k3g_mx_grouped_matmul names them
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class K3GError(RuntimeError):
@@ -47,6 +52,11 @@ class Mxfp4(C.Structure):
 
 class Expert(C.Structure):
     _fields_ = [("w1", Mxfp4), ("w3", Mxfp4), ("w2", Mxfp4)]
+
+
+class MxStruct(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int32), ("in_", C.c_int32),
+                ("format", C.c_int32)]
 
 
 class ExpertBank(C.Structure):
@@ -120,6 +130,13 @@ def lib():
         L.k3g_latent_moe_block.argtypes = [P, P, P, i, i, i, P, sz, P]
         L.k3g_quantize_i8_groups.argtypes = [P, P, P, i, i, P]
         L.k3g_mxfp4_idot_groupsums.argtypes = [P, P, P, i, i, i, P]
+        i64, f = C.c_int64, C.c_float
+        L.k3g_mx_quantize.argtypes = [P, P, i, i64, P]
+        L.k3g_mx_dequantize.argtypes = [P, i, i64, P, P]
+        L.k3g_add_rmsnorm.argtypes = [P, i64, P, i64, P, P, i64, P, i64, i, P, f, i, i, P]
+        L.k3g_mx_matmul.argtypes = [P, i, i64, P, P, P]
+        L.k3g_mx_grouped_matmul.argtypes = [P, i, i64, P, P, i, P, P, i, i, P]
+        L.k3g_mx_grouped_glu.argtypes = [P, P, P, P, P, i, i, P]
         L.k3g_probe_mfma_rate.argtypes = [i, i, P, P]
         L.k3g_probe_read_rate.argtypes = [P, sz, P, P]
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
@@ -193,7 +210,9 @@ def mxfp4(packed: torch.Tensor, scales: torch.Tensor) -> Mxfp4:
     rows, half = packed.shape
     if scales.shape != (rows, half * 2 // GROUP):
         raise ValueError("scales must be [rows, in/32]")
-    return Mxfp4(packed.data_ptr(), scales.data_ptr(), rows, half * 2)
+    m = Mxfp4(packed.data_ptr(), scales.data_ptr(), rows, half * 2)
+    m._keep = (packed, scales)  # the struct holds raw device pointers: keep the tensors alive with it
+    return m
 
 
 def expert_struct(ex: dict) -> Expert:
@@ -418,6 +437,182 @@ def k3g_mxfp4_idot_groupsums(sums: torch.Tensor, q: torch.Tensor, packed: torch.
     _check("k3g_mxfp4_idot_groupsums", lib().k3g_mxfp4_idot_groupsums(_ptr(sums), _ptr(q), _ptr(packed), n_in,
                                                                        rows, T, _stream(stream)))
     return sums
+
+
+# ---- microscaled activations -------------------------------------------------
+
+class Mx:
+    """A microscaled matrix (k3g_mx): codes uint8 [rows, in/2] (MXFP4) or
+    [rows, in] (MXFP8), scales uint8 [rows, in/32], and their format."""
+
+    __slots__ = ("codes", "scales", "format", "rows", "n_in", "struct")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int):
+        if fmt not in (MXFP4, MXFP8):
+            raise ValueError("format must be MXFP4 or MXFP8")
+        _dev(codes, torch.uint8, "codes")
+        _dev(scales, torch.uint8, "scales")
+        if codes.dim() != 2:
+            raise ValueError("codes must be [rows, in/2] (MXFP4) or [rows, in] (MXFP8)")
+        self.rows, self.n_in = codes.shape[0], codes.shape[1] * (2 if fmt == MXFP4 else 1)
+        if self.n_in % GROUP or tuple(scales.shape) != (self.rows, self.n_in // GROUP):
+            raise ValueError("scales must be [rows, in/32]")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.format = codes, scales, fmt
+        self.struct = MxStruct(codes.data_ptr(), scales.data_ptr(), self.rows, self.n_in, fmt)
+
+
+def mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int) -> Mx:
+    """The microscaled matrix of these tensors."""
+    return Mx(codes, scales, fmt)
+
+
+def mx_empty(rows: int, n_in: int, fmt: int, device="cuda") -> Mx:
+    """A microscaled matrix of that size, not initialised."""
+    if fmt not in (MXFP4, MXFP8) or rows < 0 or n_in <= 0 or n_in % GROUP:
+        raise ValueError("invalid microscaled shape or format")
+    return Mx(torch.empty((rows, n_in // 2 if fmt == MXFP4 else n_in), dtype=torch.uint8, device=device),
+              torch.empty((rows, n_in // GROUP), dtype=torch.uint8, device=device), fmt)
+
+
+def _rows(t: torch.Tensor, name: str, shape=None, dtype=None):
+    """A dense operand [rows, cols]: rows may lie apart, entries may not. Returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {list(shape) if shape else '[rows, cols]'}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have its entries side by side")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return t.stride(0)
+
+
+def _here(*tensors):
+    """The launch goes to the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _mx_arg(q, name: str) -> Mx:
+    if not isinstance(q, Mx):
+        raise TypeError(f"{name} must be an Mx (see mx and mx_empty)")
+    return q
+
+
+def k3g_mx_quantize(q: Mx, x: torch.Tensor, stream=None) -> Mx:
+    """x [rows, in] (float32, bfloat16 or float16; rows may lie apart) -> q, per 32-group."""
+    _mx_arg(q, "q")
+    ld = _rows(x, "x", (q.rows, q.n_in))
+    _here(x, q.codes)
+    _check("k3g_mx_quantize", lib().k3g_mx_quantize(C.byref(q.struct), x.data_ptr(), _TYPES[x.dtype], ld,
+                                                     _stream(stream)))
+    return q
+
+
+def k3g_mx_dequantize(y: torch.Tensor, q: Mx, stream=None) -> torch.Tensor:
+    """q's values, rounded once to y's type."""
+    _mx_arg(q, "q")
+    ld = _rows(y, "y", (q.rows, q.n_in))
+    _here(y, q.codes)
+    _check("k3g_mx_dequantize", lib().k3g_mx_dequantize(y.data_ptr(), _TYPES[y.dtype], ld, C.byref(q.struct),
+                                                         _stream(stream)))
+    return y
+
+
+def k3g_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, r: torch.Tensor | None = None,
+                    sum: torch.Tensor | None = None, y: torch.Tensor | None = None, q: Mx | None = None,
+                    stream=None):
+    """s = x + r (r None: x); sum = s, y = s / sqrt(mean(s^2) + eps) * gamma and q = y quantised, each where
+    given (at least one of y and q). sum or y may be x or r itself. Returns (sum, y, q)."""
+    ld = _rows(x, "x")
+    n, n_in = x.shape
+    _dev(gamma, torch.float32, "gamma")
+    if gamma.numel() != n_in:
+        raise ValueError("gamma must have one entry a column")
+    if y is None and q is None:
+        raise ValueError("at least one of y and q")
+    one = {}
+    for name, t in (("r", r), ("sum", sum), ("y", y)):
+        one[name] = (t.data_ptr(), _rows(t, name, (n, n_in), x.dtype)) if t is not None else (None, 0)
+    if q is not None and (_mx_arg(q, "q").rows, q.n_in) != (n, n_in):
+        raise ValueError("q must have x's rows and columns")
+    _here(x, gamma, r, sum, y, None if q is None else q.codes)
+    _check("k3g_add_rmsnorm", lib().k3g_add_rmsnorm(*one["y"], *one["sum"], None if q is None else C.byref(q.struct),
+                                                     x.data_ptr(), ld, *one["r"], _TYPES[x.dtype], gamma.data_ptr(),
+                                                     eps, n, n_in, _stream(stream)))
+    return sum, y, q
+
+
+def k3g_mx_matmul(y: torch.Tensor, a: Mx, w: Mxfp4, stream=None) -> torch.Tensor:
+    """y [rows of a, rows of w] = a w^T on the block-scaled matrix cores (w from mxfp4())."""
+    _mx_arg(a, "a")
+    if w.in_ != a.n_in:
+        raise ValueError("shape mismatch")
+    ld = _rows(y, "y", (a.rows, w.rows))
+    _here(y, a.codes, *getattr(w, "_keep", ()))
+    _check("k3g_mx_matmul", lib().k3g_mx_matmul(y.data_ptr(), _TYPES[y.dtype], ld, C.byref(a.struct), C.byref(w),
+                                                 _stream(stream)))
+    return y
+
+
+def _groups(a: Mx, bank: ExpertBank, offsets: torch.Tensor, perm, top_k: int, n_rows: int):
+    _dev(offsets, torch.int32, "offsets")
+    if offsets.numel() != bank.n_experts + 1:
+        raise ValueError("offsets must have n_experts + 1 entries")
+    if perm is not None:
+        _dev(perm, torch.int32, "perm")
+        if perm.numel() != n_rows:
+            raise ValueError("perm must have an entry a row")
+    elif a.rows < n_rows:
+        raise ValueError("without perm, a must have a row for each row of the output")
+    if top_k < 1:
+        raise ValueError("top_k must be positive")
+    _here(a.codes, offsets, perm, getattr(bank, "_keep", None))
+
+
+def k3g_mx_grouped_matmul(y: torch.Tensor, a: Mx, bank: ExpertBank, tensor: int, offsets: torch.Tensor,
+                          perm: torch.Tensor | None = None, top_k: int = 1, stream=None) -> torch.Tensor:
+    """y[p] = W_e a[p] (or a[perm[p] // top_k]) for the rows p of each expert e's group, offsets[e] ..
+    offsets[e + 1] - 1; W: the bank's tensor W1, W3 or W2. Rows outside the groups are left as they were."""
+    _mx_arg(a, "a")
+    if tensor not in (W1, W3, W2):
+        raise ValueError("tensor must be W1, W3 or W2")
+    rows, cols = (bank.latent, bank.inter) if tensor == W2 else (bank.inter, bank.latent)
+    ld = _rows(y, "y")
+    if y.shape[1] != rows or a.n_in != cols:
+        raise ValueError("shape mismatch")
+    _groups(a, bank, offsets, perm, top_k, y.shape[0])
+    _here(y)
+    _check("k3g_mx_grouped_matmul", lib().k3g_mx_grouped_matmul(
+        y.data_ptr(), _TYPES[y.dtype], ld, C.byref(a.struct), C.byref(bank), tensor, offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), top_k, y.shape[0], _stream(stream)))
+    return y
+
+
+def k3g_mx_grouped_glu(h: Mx, a: Mx, bank: ExpertBank, offsets: torch.Tensor, perm: torch.Tensor | None = None,
+                       top_k: int = 1, stream=None) -> Mx:
+    """h[p] = SiTU(w1 a, w3 a) of each row's expert, quantised per 32-group; rows and groups as
+    k3g_mx_grouped_matmul."""
+    _mx_arg(h, "h")
+    _mx_arg(a, "a")
+    if h.n_in != bank.inter or a.n_in != bank.latent:
+        raise ValueError("shape mismatch")
+    _groups(a, bank, offsets, perm, top_k, h.rows)
+    _here(h.codes)
+    _check("k3g_mx_grouped_glu", lib().k3g_mx_grouped_glu(
+        C.byref(h.struct), C.byref(a.struct), C.byref(bank), offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), top_k, h.rows, _stream(stream)))
+    return h
 
 
 # ---- bank packing (data placement only) -------------------------------------
