@@ -22,7 +22,7 @@ struct MmArgs {
     int E, top_k;
     int y_type, y_vec;  // y_vec: four outputs are one aligned store
     int h_format;
-    int two;  // some row's scale bytes of a step straddle aligned dwords
+    int odd;  // some row's scale bytes lie off 16-byte addresses, or its groups end inside sixteen
 };
 
 // One step of 128 entries. The matrix cores add products of unlike magnitude
@@ -72,28 +72,43 @@ __device__ inline uint4 keep4(const uint4 &v, bool keep) {
 
 enum { DENSE = 0, GROUPED = 1, GLU = 2 };
 
-__device__ inline void store4(const MmArgs &a, int64_t token, int row, const float4_t &v) {
-    if (row >= a.rows) return;
-    const int64_t at = token * a.ys + row;
-    if (a.y_vec && row + 4 <= a.rows) {
-        if (a.y_type == K3G_F32)
-            *(float4_t *)((float *)a.y + at) = v;
-        else if (a.y_type == K3G_BF16)
-            store_n<K3G_BF16, 4>((__bf16 *)__builtin_assume_aligned((__bf16 *)a.y + at, 8), (const float *)&v);
-        else
-            store_n<K3G_F16, 4>((_Float16 *)__builtin_assume_aligned((_Float16 *)a.y + at, 8), (const float *)&v);
-        return;
-    }
+// Four consecutive outputs of one token, at element `at` of y; the first `n` of
+// them exist (n below 4 only without VEC: there, rows are a multiple of 4).
+template <int TYPE, bool VEC>
+__device__ inline void store4(void *y, int64_t at, int n, const float4_t &v) {
+    typedef typename Elem<TYPE>::T T;
+    T *p = (T *)y + at;
+    if (n <= 0) return;
+    if constexpr (VEC) {
+        store_n<TYPE, 4>((T *)__builtin_assume_aligned(p, 4 * sizeof(T)), (const float *)&v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (row + i >= a.rows) break;
-        if (a.y_type == K3G_F32)
-            ((float *)a.y)[at + i] = v[i];
-        else if (a.y_type == K3G_BF16)
-            ((__bf16 *)a.y)[at + i] = (__bf16)v[i];
-        else
-            ((_Float16 *)a.y)[at + i] = (_Float16)v[i];
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = Elem<TYPE>::store(v[i]);
     }
+}
+
+// f(store) with store = store4 for y's type and alignment (uniform).
+template <class F>
+__device__ inline void with_store(const MmArgs &a, F f) {
+#define K3G_STORE(TYPE, VEC) \
+    f([&](int64_t at, int n, const float4_t &v) { store4<TYPE, VEC>(a.y, at, n, v); })
+    if (a.y_vec) {
+        if (a.y_type == K3G_F32)
+            K3G_STORE(K3G_F32, true);
+        else if (a.y_type == K3G_BF16)
+            K3G_STORE(K3G_BF16, true);
+        else
+            K3G_STORE(K3G_F16, true);
+    } else {
+        if (a.y_type == K3G_F32)
+            K3G_STORE(K3G_F32, false);
+        else if (a.y_type == K3G_BF16)
+            K3G_STORE(K3G_BF16, false);
+        else
+            K3G_STORE(K3G_F16, false);
+    }
+#undef K3G_STORE
 }
 
 // A 32-group of h of one token, spread over the four lanes r + 16q: lane q

@@ -108,7 +108,8 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
             }
         } else if (wave < 2) {
             const float4_t s = sum(wave);
-            if (r < n_tok) store4(a, p + r, row0 + 16 * wave + 4 * q, s);
+            const int row = row0 + 16 * wave + 4 * q;
+            if (r < n_tok) with_store(a, [&](auto store) { store((p + r) * a.ys + row, a.rows - row, s); });
         }
         __syncthreads();  // part is read before the next tile writes it
     }
@@ -170,14 +171,14 @@ int groups_ok(const k3g_mx *a, const int32_t *offsets, const int32_t *perm, int 
     return K3G_OK;
 }
 
-int y_vec(const void *y, int type, int64_t stride) {
-    return mx_aligned(y, 4 * type_size(type)) && stride % 4 == 0;
+int y_vec(const void *y, int type, int64_t stride, int rows) {
+    return mx_aligned(y, 4 * type_size(type)) && stride % 4 == 0 && rows % 4 == 0;
 }
 
-// Whether four scale bytes of some row and step straddle aligned dwords.
-int straddle(const MmArgs &m) {
+// Whether some row's scale bytes lie off 16-byte addresses, or end inside sixteen.
+int odd_scales(const MmArgs &m) {
     const uintptr_t bits = (uintptr_t)m.a_scales | (uintptr_t)m.ws[0] | (uintptr_t)m.ws[1] | (uintptr_t)m.G;
-    return (bits & 3) != 0;
+    return (bits & 15) != 0;
 }
 
 }  // namespace
@@ -203,9 +204,9 @@ int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const 
     MmArgs m = {};
     m.a_codes = a->codes, m.a_scales = a->scales, m.a_rows = a->rows;
     m.w[0] = w->packed, m.ws[0] = w->scales;
-    m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride);
+    m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, w->rows);
     m.T = a->rows, m.rows = w->rows, m.in = a->in, m.G = a->in / kGroup;
-    m.two = straddle(m);
+    m.odd = odd_scales(m);
     return launch_stream<DENSE>(m, a->format, (hipStream_t)stream);
 }
 
@@ -231,9 +232,9 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
     K3G_TRY(device_ok());
     m.a_codes = a->codes, m.a_scales = a->scales, m.a_rows = a->rows;
     m.stride = bank->stride, m.offsets = offsets, m.perm = perm, m.top_k = top_k, m.E = bank->n_experts;
-    m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride);
+    m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, d.rows);
     m.T = n_rows, m.rows = d.rows, m.in = d.in, m.G = d.in / kGroup;
-    m.two = straddle(m);
+    m.odd = odd_scales(m);
     return launch_stream<GROUPED>(m, a->format, (hipStream_t)stream);
 }
 
@@ -265,7 +266,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
     m.stride = bank->stride, m.offsets = offsets, m.perm = perm, m.top_k = top_k, m.E = bank->n_experts;
     m.h_codes = h->codes, m.h_scales = h->scales, m.h_format = h->format;
     m.T = n_rows, m.rows = bank->inter, m.in = bank->latent, m.G = bank->latent / kGroup;
-    m.two = straddle(m);
+    m.odd = odd_scales(m);
     return launch_stream<GLU>(m, a->format, (hipStream_t)stream);
 }
 

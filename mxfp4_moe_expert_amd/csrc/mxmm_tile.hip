@@ -6,11 +6,13 @@
 // token, written by LDS DMA: four (eight) consecutive lanes take one row's
 // contiguous bytes, 16-byte chunk c of row i at place c ^ (i/2 % 4) (c ^ i % 8),
 // so that the operand reads (16 bytes of 16 rows a quarter wavefront) meet no
-// bank twice. The rows' scale bytes come as aligned dwords the same way. The
-// wavefront that loaded a row turns its four bytes of a stage into operand order
-// (one dword a lane for four operand tiles: the instruction picks the byte),
-// and where one is 255 or past the row's end it zeroes the group's codes in LDS
-// and makes the scale finite.
+// bank twice. Scales come for four stages at a time, 16 bytes a row: one lane a
+// row, whatever the width of the request, so a request a stage would cost the
+// address unit as much as the data. The wavefront that loaded a row turns its
+// bytes into operand order (for each group of a step one dword, a byte for each
+// of the four stages: the instruction picks the byte), and where one is 255 or
+// past the row's end it makes the scale finite and, when the stage has landed,
+// zeroes the group's codes in LDS.
 //
 // Pipeline, one barrier a stage, in the middle of its products:
 //   products of stage s, first half | wait for the own rows of s+1, prepare them
@@ -23,26 +25,37 @@
 
 namespace k3g {
 
-template <int AF, int MODE_, int WR_, int WC_, int FM_, int FN_, int NB_>
+// WR x WC wavefronts of FM x FN operand tiles (16 x 16) each, NB stages in LDS.
+// ODD: rows whose scale bytes start off 16-byte addresses or end inside four
+// stages; they come as five aligned dwords and are shifted into place.
+template <int AF, int MODE_, int WR_, int WC_, int FM_, int FN_, int NB_, bool ODD_>
 struct Tile {
     static constexpr int MODE = MODE_, WR = WR_, WC = WC_, FM = FM_, FN = FN_, NB = NB_;
+    static constexpr bool ODD = ODD_;
     static constexpr int NW = WR * WC, THREADS = NW * kWave;
     static constexpr int BM = WR * FM * 16, BN = WC * FN * 16;
     static constexpr int OUT = MODE == GLU ? BM / 2 : BM;  // outputs of a tile
     static constexpr int AB = AF == K3G_MXFP4 ? 64 : 128;  // bytes of a token a stage
-    static constexpr int MW = BM / NW, MA = BN / NW;       // rows that a wavefront loads
+    static constexpr int MW = BM / NW, MA = BN / NW;       // rows that a wavefront loads and prepares
     static constexpr int DW = MW / 16, DA = MA * AB / 1024;  // DMA instructions of 1 KB
-    static constexpr int SW = (MW + 63) / 64, SA = (MA + 63) / 64;  // scale DMA instructions (one dword a row)
-    static_assert(MW % 16 == 0 && MA % 16 == 0 && MW <= 64 && MA <= 64, "rows per wavefront");
-    static_assert((FM % 4 == 0 || 4 % FM == 0) && (FN % 4 == 0 || 4 % FN == 0), "scale dwords");
-    static_assert(MODE != GLU || FM % 4 == 0, "a wavefront owns whole 32-groups of h");
-    static constexpr int V1 = DW + DA + 2;  // loads in flight per stage, scales in aligned dwords
-    static constexpr int V2 = V1 + 2;       // scales that straddle dwords: two a row
-    // LDS: data and raw scales per stage, operand-order scales (two stages)
-    static constexpr int DATA = BM * 64 + BN * AB, RAW = (BM + BN) * 8, STAGE = DATA + RAW;
-    static constexpr int SCALES = (BM + BN) * 4;
-    static constexpr int TABLE = NB * STAGE + 2 * SCALES;  // then the grouped form's table
+    static_assert(MW % 16 == 0 && MA % 16 == 0 && MW + MA <= kWave, "a lane for each row of a wavefront");
+    static_assert(FM % 4 == 0 && FN % 2 == 0, "halves; GLU: a wavefront owns whole 32-groups of h");
+    static constexpr int V = DW + DA, X = ODD ? 5 : 1;  // loads of a stage, and of four stages' scales
+    static_assert(NB >= 2 && NB <= 4, "the scales of four stages are prepared before the next four's are loaded");
+    // LDS: data per stage, raw scales of four stages, scales in operand order
+    static constexpr int STAGE = BM * 64 + BN * AB, RAW_W = kWave * (ODD ? 20 : 16), RAW = NW * RAW_W;
+    static constexpr int SCALES = (BM + BN) * 16;
+    static constexpr int RAW_AT = NB * STAGE, SCALES_AT = RAW_AT + RAW;
+    static constexpr int TABLE = SCALES_AT + SCALES;  // then the grouped form's table
     static constexpr int lds(int E) { return TABLE + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
+    static constexpr int WGS = lds(900) <= 81920 ? 2 : 1;
+    // loads in flight behind stage s+1 (s % 4 = ph): stages s+2 .. s+NB-1
+    static constexpr int behind(int ph) {
+        int n = (NB - 2) * V;
+        for (int k = 2; k < NB; ++k)
+            if ((ph + k) % 4 == 0) n += X;
+        return n;
+    }
 };
 
 __device__ inline void stage_barrier() {
@@ -55,18 +68,9 @@ __device__ inline void dma4_at(const void *p, uint32_t lds) {
     __asm__ volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(p), "s"(lds) : "m0");
 }
 
-// Waits until at most K stages' loads are in flight, of the `left` stages that
-// follow the one waited for (fewer near the end of the row: all of them).
-template <int V1, int V2, int K>
-__device__ inline void wait_stages(bool two, int left) {
-    if (left >= K) {
-        if (two)
-            wait_vm<K * V2 < 64 ? K * V2 : 63>();
-        else
-            wait_vm<K * V1>();
-    } else {
-        wait_vm<0>();
-    }
+__device__ inline void dma16_at(const void *p, uint32_t lds) {
+    lds = __builtin_amdgcn_readfirstlane(lds);
+    __asm__ volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds) : "m0");
 }
 
 // Operand tiles i0 .. i1-1 of the weights with every token tile. The loops are
@@ -81,7 +85,8 @@ struct MakeSeq<0, I...> {
     typedef Seq<I...> type;
 };
 
-template <int AF, class C, int J, int I0, int... I>
+// (w: the half's tiles; sw, st: a byte of each stage in turn, PH the stage's.)
+template <int AF, class C, int PH, int J, int I0, int... I>
 __device__ inline void mul_column(const uint4 *w, const uint4 *t, const uint32_t *sw, uint32_t st,
                                   float4_t (*acc)[C::FN], Seq<I...>) {
     const Act<AF> b = [&] {
@@ -90,27 +95,32 @@ __device__ inline void mul_column(const uint4 *w, const uint4 *t, const uint32_t
         else
             return Act<AF>(t[0], t[1]);
     }();
-    ((acc[I0 + I][J] = b.template mul<(I0 + I) & 3, J & 3>(
-          v8i_t{(int)w[I0 + I].x, (int)w[I0 + I].y, (int)w[I0 + I].z, (int)w[I0 + I].w, 0, 0, 0, 0}, acc[I0 + I][J],
-          sw[(I0 + I) / 4], st)),
+    ((acc[I0 + I][J] =
+          b.template mul<PH, PH>(v8i_t{(int)w[I].x, (int)w[I].y, (int)w[I].z, (int)w[I].w, 0, 0, 0, 0},
+                                 acc[I0 + I][J], sw[I0 + I], st)),
      ...);
 }
-template <int AF, class C, int I0, int N, int... J>
+// Token tiles J0 + J... with the weights' tiles I0 .. I0+NI-1 (w, t: those tiles).
+template <int AF, class C, int PH, int I0, int NI, int J0, int... J>
 __device__ inline void mul_tiles(const uint4 *w, const uint4 (*t)[C::AB / 64], const uint32_t *sw, const uint32_t *st,
                                  float4_t (*acc)[C::FN], Seq<J...>) {
-    (mul_column<AF, C, J, I0>(w, t[J], sw, st[J / 4], acc, typename MakeSeq<N>::type{}), ...);
+    (mul_column<AF, C, PH, J0 + J, I0>(w, t[J], sw, st[J0 + J], acc, typename MakeSeq<NI>::type{}), ...);
 }
 
-template <int H>
-struct Half {
-    static constexpr int value = H;
+template <int H_, int Q_>
+struct Part {
+    static constexpr int H = H_, Q = Q_;
+};
+template <int PH_>
+struct Phase {
+    static constexpr int PH = PH_;
 };
 
 template <int AF, class C>
-__global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile_kernel(MmArgs a) {
     extern __shared__ __align__(1024) uint8_t lds[];
-    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r = lane & 15, q = lane >> 4;
+    int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wr = wave / C::WC, wc = wave % C::WC;
     const uint32_t lds0 = lds_addr(lds);
     const int n_rb = (a.rows + C::OUT - 1) / C::OUT;
@@ -156,7 +166,20 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
     const int xcd = blockIdx.x % 8, step = gridDim.x / 8;
     const int64_t last = n_items * (xcd + 1) / 8;
     for (int64_t item = n_items * xcd / 8 + blockIdx.x / 8; item < last; item += step) {
-        const int tile = (int)(item / n_rb), m0 = (int)(item % n_rb) * C::OUT;
+        int tile, rb;
+        if constexpr (C::MODE == DENSE) {
+            // token tiles in groups of four, row block by row block: the
+            // workgroups of an XCD that run together read 4 token tiles and a
+            // quarter as many row blocks as there are of them
+            const int64_t group = item / (4 * n_rb), in_group = item - group * 4 * n_rb;
+            const int wide = min(4, n_tiles - (int)group * 4);
+            rb = (int)in_group / wide;
+            tile = (int)group * 4 + (int)in_group % wide;
+        } else {
+            tile = (int)(item / n_rb);
+            rb = (int)(item % n_rb);
+        }
+        const int m0 = rb * C::OUT;
         int e = 0, p, end;
         if constexpr (C::MODE == DENSE) {
             p = tile * C::BN;
@@ -178,6 +201,9 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
         }
         const int n_tok = min(C::BN, end - p);
 
+        // what depends on the lane is computed again for each item, and again for the way out:
+        // kept across the products it would not fit the registers
+        __asm__ volatile("" : "+v"(lane));
         // ---- what this wavefront loads: MW weight rows from row MW * wave, MA tokens from MA * wave
         const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
         // row i of the tile's weights: tensor and row past m0
@@ -191,7 +217,6 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
         uint32_t vw[C::DW], va[C::DA];
         const uint8_t *bw[C::DW];
         const uint8_t *ba = a.perm ? a.a_codes : a.a_codes + (int64_t)p * a_pitch;
-        const uint8_t *bsa = a.perm ? a.a_scales : a.a_scales + (int64_t)p * a.G;
         auto a_row = [&](int i) {  // row of the activations past ba
             const int t = min(i, n_tok - 1);
             return a.perm ? source_row(a, p + t) : t;
@@ -206,20 +231,17 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
 #pragma unroll
         for (int d = 0; d < C::DA; ++d)
             va[d] = (uint32_t)a_row(wave * C::MA + RA * d + lane / (64 / RA)) * a_pitch + 16 * ca;
-        // scales: this lane's weight row and token (lanes past the wavefront's rows idle)
-        const int iw = wave * C::MW + min(lane, C::MW - 1), ia = wave * C::MA + min(lane, C::MA - 1);
-        const uint8_t *bsw = a.ws[0] + e * a.stride + (int64_t)m0 * a.G;
-        uint64_t w_off = (uint64_t)w_row(iw) * a.G;
-        if (C::MODE == GLU && w_tensor(iw)) w_off += a.ws[1] - a.ws[0];
-        // addresses cut to dwords; `two`: some row's four bytes straddle dwords
-        const uint64_t aw = (uint64_t)bsw + w_off, aa = (uint64_t)bsa + (uint64_t)a_row(ia) * a.G;
-        const int shw = (int)(aw & 3), sha = (int)(aa & 3);
-        const bool two = a.two;
+        // the row whose scales this lane loads and prepares: a weight row, from lane MW on a token
+        const bool is_w = lane < C::MW, has_row = lane < C::MW + C::MA;
+        const int iw = wave * C::MW + min(lane, C::MW - 1);
+        const int ia = wave * C::MA + min(max(lane - C::MW, 0), C::MA - 1);
+        const uint64_t s_addr =
+            is_w ? (uint64_t)(a.ws[w_tensor(iw)] + e * a.stride) + (uint64_t)(m0 + w_row(iw)) * a.G
+                 : (uint64_t)a.a_scales + ((uint64_t)(a.perm ? 0 : p) + (uint64_t)a_row(ia)) * a.G;
         const int S = (a.G + 3) / 4, Gt = a.G - 4 * (S - 1);  // stages, groups of the last
 
-        auto issue = [&](int s) {
-            const uint32_t buf = lds0 + (uint32_t)(s % C::NB) * C::STAGE;
-            const bool tail = s == S - 1;
+        auto issue = [&](int s, int buffer, bool tail) {
+            const uint32_t buf = lds0 + (uint32_t)buffer * C::STAGE;
             // past the row's end the last whole chunk is read again (its place is zeroed later)
             const uint32_t backw = tail ? 16u * (uint32_t)max(cw - (Gt - 1), 0) : 0u;
             const uint32_t backa =
@@ -230,96 +252,109 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
 #pragma unroll
             for (int d = 0; d < C::DA; ++d)
                 dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + wave * C::MA * C::AB + 1024 * d);
-            const uint32_t raw = buf + C::DATA;
-            const int need = tail ? Gt - 1 : 3;
-            const uint64_t w4 = aw + 4 * (uint64_t)s, a4 = aa + 4 * (uint64_t)s;
-            if (lane < C::MW) {
-                dma4_at((const void *)(w4 & ~3ull), raw + wave * C::MW * 4);
-                if (two) dma4_at((const void *)((w4 + need) & ~3ull), raw + (C::BM + wave * C::MW) * 4);
-            }
-            if (lane < C::MA) {
-                dma4_at((const void *)(a4 & ~3ull), raw + (2 * C::BM + wave * C::MA) * 4);
-                if (two) dma4_at((const void *)((a4 + need) & ~3ull), raw + (2 * C::BM + C::BN + wave * C::MA) * 4);
-            }
         };
-
-        // this wavefront's rows of stage s, landed: scales to operand order, groups that add nothing zeroed
-        auto prepare = [&](int s) {
-            uint8_t *buf = lds + (s % C::NB) * C::STAGE;
-            uint8_t *sc = lds + C::NB * C::STAGE + (s & 1) * C::SCALES;
-            const uint32_t *raw = (const uint32_t *)(buf + C::DATA);
-            const int n = s == S - 1 ? Gt : 4;
-            const uint32_t past = n == 4 ? 0u : ~0u << (8 * n);
-            uint32_t dw = raw[iw], da = raw[2 * C::BM + ia];
-            if (two) {
-                dw = __builtin_amdgcn_alignbyte(raw[C::BM + iw], dw, shw);
-                da = __builtin_amdgcn_alignbyte(raw[2 * C::BM + C::BN + ia], da, sha);
-            }
-            dw |= past;
-            da |= past;
-            // bytes equal to 255: the top bit of (b & 127) + 1, where b's own top bit is set
-            const uint32_t fw = ((dw & 0x7F7F7F7Fu) + 0x01010101u) & dw & 0x80808080u;
-            const uint32_t fa = ((da & 0x7F7F7F7Fu) + 0x01010101u) & da & 0x80808080u;
-            // 255 -> 127: take the top bit away
-            const uint32_t ow = dw ^ fw, oa = da ^ fa;
-            if (lane < C::MW) {
-                uint8_t *o = sc + (iw / 64) * 256 + (iw & 15) * 4 + ((iw >> 4) & 3);
+        const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
+        auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
+            if (!has_row) return;         // (lane 0 always has one)
+            const uint64_t at = s_addr + 16 * (uint64_t)u;
+            if constexpr (!C::ODD) {
+                dma16_at((const void *)at, raw);
+            } else {
+                // the aligned dwords that hold the bytes; past the row's last byte, the one that holds it
+                const uint64_t last = (s_addr + a.G - 1) & ~3ull;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[64 * k] = (uint8_t)(ow >> (8 * k));
-            }
-            if (lane < C::MA) {
-                uint8_t *o = sc + C::BM * 4 + (ia / 64) * 256 + (ia & 15) * 4 + ((ia >> 4) & 3);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[64 * k] = (uint8_t)(oa >> (8 * k));
-            }
-            if (__builtin_expect(__ballot((fw | fa) != 0) != 0, 0)) {
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (lane < C::MW && ((fw >> (8 * k)) & 0x80u))
-                        *(uint4 *)(buf + iw * 64 + 16 * (k ^ ((iw >> 1) & 3))) = zero;
-                    if (lane < C::MA && ((fa >> (8 * k)) & 0x80u)) {
-                        uint8_t *row = buf + C::BM * 64 + ia * C::AB;
-                        if constexpr (AF == K3G_MXFP4) {
-                            *(uint4 *)(row + 16 * (k ^ ((ia >> 1) & 3))) = zero;
-                        } else {
-                            *(uint4 *)(row + 16 * ((2 * k) ^ (ia & 7))) = zero;
-                            *(uint4 *)(row + 16 * ((2 * k + 1) ^ (ia & 7))) = zero;
-                        }
-                    }
+                for (int k = 0; k < 5; ++k) {
+                    const uint64_t w = (at & ~3ull) + 4 * k;
+                    dma4_at((const void *)(w < last ? w : last), raw + 256 * k);
                 }
             }
         };
 
-        // operands of a stage
-        struct Ops {
-            uint4 w[C::FM];
-            uint4 t[C::FN][C::AB / 64];
-            uint32_t sw[(C::FM + 3) / 4], st[(C::FN + 3) / 4];
+        // this wavefront's rows: the scales of the stages 4u .. to operand order, and a stage's
+        // groups that add nothing (bits in `out`, a dword a stage) zeroed
+        const int s_at = C::SCALES_AT + 16 * (is_w ? iw : C::BM + ia);
+        const int d_at = is_w ? iw * 64 : C::BM * 64 + ia * C::AB;
+        const int d_swz = is_w ? (iw >> 1) & 3 : AF == K3G_MXFP4 ? (ia >> 1) & 3 : ia & 7;
+        uint32_t out[4];
+        auto prepare_scales = [&](int u) {
+            uint32_t d[4];
+            if constexpr (!C::ODD) {
+                const uint4 v = *(const uint4 *)(lds + C::RAW_AT + wave * C::RAW_W + 16 * lane);
+                d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+            } else {
+                const uint32_t *v = (const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W) + lane;
+                uint32_t lo = v[0];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t hi = v[64 * (k + 1)];
+                    d[k] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)s_addr & 3u);
+                    lo = hi;
+                    const int left = a.G - 16 * u - 4 * k;  // groups from this stage on
+                    if (left < 4) d[k] |= left > 0 ? ~0u << (8 * left) : ~0u;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // bytes equal to 255: b's top bit, where (b & 127) + 1 has it too; they become 127
+                const uint32_t f = ((d[k] & 0x7F7F7F7Fu) + 0x01010101u) & d[k] & 0x80808080u;
+                d[k] ^= f;
+                out[k] = has_row ? f : 0u;
+            }
+            // [stage][group] bytes -> [group][stage]
+            const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u);  // 0: 0,0 1,0 0,1 1,1
+            const uint32_t a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+            const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
+            const uint32_t b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+            const uint4 o = make_uint4(__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                                       __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u));
+            if (has_row) *(uint4 *)(lds + s_at) = o;
         };
+        auto zero_groups = [&](uint32_t f, int buffer) {
+            while (__ballot(f != 0) != 0) {  // rarely entered; a group a round
+                if (f) {
+                    const int k = __builtin_ctz(f) >> 3;
+                    uint8_t *row = lds + buffer * C::STAGE + d_at;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    if (AF == K3G_MXFP4 || is_w) {
+                        *(uint4 *)(row + 16 * (k ^ d_swz)) = zero;
+                    } else {
+                        *(uint4 *)(row + 16 * ((2 * k) ^ d_swz)) = zero;
+                        *(uint4 *)(row + 16 * ((2 * k + 1) ^ d_swz)) = zero;
+                    }
+                    f &= f - 1;
+                }
+            }
+        };
+
+        // Operands of a stage in two halves: by weight rows, the tokens' tiles whole and
+        // in two sets (now, next), or by tokens with the weights' whole: an e4m3
+        // tile is cut in two for the matrix cores, which is done once that way.
+        constexpr bool BY_ROWS = AF == K3G_MXFP4;
+        constexpr int HM = BY_ROWS ? C::FM / 2 : C::FM, HN = BY_ROWS ? C::FN : C::FN / 2;
+        uint4 wt[2][HM], tk[2][HN][C::AB / 64];
+        uint32_t sw[C::FM], st[C::FN];
+        const int r = lane & 15, q = lane >> 4;
         const int w_at = (wr * C::FM * 16 + r) * 64 + 16 * (q ^ ((r >> 1) & 3));
         const int a_at = C::BM * 64 + (wc * C::FN * 16 + r) * C::AB +
                          16 * (AF == K3G_MXFP4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7));
-        auto read = [&](Ops &o, int s) {
-            const uint8_t *buf = lds + (s % C::NB) * C::STAGE;
-            const uint8_t *sc = lds + C::NB * C::STAGE + (s & 1) * C::SCALES + q * 64 + r * 4;
+        auto read_w = [&](uint4 *o, int buffer, int half) {
 #pragma unroll
-            for (int k = 0; k < (C::FM + 3) / 4; ++k) {
-                const int f = wr * C::FM + 4 * k;
-                o.sw[k] = *(const uint32_t *)(sc + (f / 4) * 256) >> (8 * (f & 3));
-            }
+            for (int i = 0; i < HM; ++i)
+                o[i] = *(const uint4 *)(lds + buffer * C::STAGE + w_at + (half * HM + i) * 1024);
+        };
+        auto read_t = [&](uint4(*o)[C::AB / 64], int buffer, int half) {
 #pragma unroll
-            for (int k = 0; k < (C::FN + 3) / 4; ++k) {
-                const int f = wc * C::FN + 4 * k;
-                o.st[k] = *(const uint32_t *)(sc + C::BM * 4 + (f / 4) * 256) >> (8 * (f & 3));
-            }
-#pragma unroll
-            for (int f = 0; f < C::FN; ++f)
+            for (int f = 0; f < HN; ++f)
 #pragma unroll
                 for (int k = 0; k < C::AB / 64; ++k)
-                    o.t[f][k] = *(const uint4 *)(buf + (a_at ^ (64 * k)) + f * 16 * C::AB);
+                    o[f][k] = *(const uint4 *)(lds + buffer * C::STAGE + (a_at ^ (64 * k)) + (half * HN + f) * 16 * C::AB);
+        };
+        auto read_s = [&] {
+            const uint8_t *sc = lds + C::SCALES_AT + 16 * r + 4 * q;
 #pragma unroll
-            for (int f = 0; f < C::FM; ++f) o.w[f] = *(const uint4 *)(buf + w_at + f * 1024);
+            for (int i = 0; i < C::FM; ++i) sw[i] = *(const uint32_t *)(sc + (wr * C::FM + i) * 256);
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) st[j] = *(const uint32_t *)(sc + C::BM * 16 + (wc * C::FN + j) * 256);
         };
 
         float4_t acc[C::FM][C::FN];
@@ -327,42 +362,84 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-        auto multiply = [&](const Ops &o, auto half) {
-            mul_tiles<AF, C, decltype(half)::value * (C::FM / 2), C::FM / 2>(o.w, o.t, o.sw, o.st, acc,
-                                                                             typename MakeSeq<C::FN>::type{});
-        };
-        const int ahead = min(C::NB, S);
-        for (int s = 0; s < ahead; ++s) issue(s);
-        wait_stages<C::V1, C::V2, C::NB - 1>(two, S - 1);
-        prepare(0);
+
+        issue_scales(0);
+        for (int s = 0; s < C::NB && s < S; ++s) issue(s, s, s == S - 1);
+        if (S >= C::NB)
+            wait_vm<(C::NB - 1) * C::V>();
+        else
+            wait_vm<0>();
+        prepare_scales(0);
+        zero_groups(out[0], 0);
         stage_barrier();
-        Ops ops[2];
-        read(ops[0], 0);
-        auto stage = [&](int s, Ops &now, Ops &next) {
-            if (s + 1 < S) {
-                // in flight behind s+1: stages up to s + NB - 1
-                wait_stages<C::V1, C::V2, C::NB - 2>(two, S - 2 - s);
-                prepare(s + 1);
+        read_s();
+        read_w(wt[0], 0, 0);
+        read_t(tk[0], 0, 0);
+        int at = 0;  // the buffer of stage s
+        // a quarter of a stage's products: half H, part Q
+        auto multiply = [&](auto phase, auto part) {
+            constexpr int PH = decltype(phase)::PH, H = decltype(part)::H, Q = decltype(part)::Q;
+            if constexpr (BY_ROWS) {
+                constexpr int N0 = C::FN / 2, J0 = Q * N0, N = Q ? C::FN - N0 : N0;
+                mul_tiles<AF, C, PH, H * HM, HM, J0>(wt[H], tk[PH & 1] + J0, sw, st, acc, typename MakeSeq<N>::type{});
+            } else {
+                constexpr int N0 = (HN + 1) / 2, J0 = Q * N0, N = Q ? HN - N0 : N0;
+                mul_tiles<AF, C, PH, 0, HM, H * HN + J0>(wt[PH & 1], tk[H] + J0, sw, st, acc,
+                                                         typename MakeSeq<N>::type{});
             }
-            multiply(now, Half<0>{});
-            if (s + 1 < S) {
-                stage_barrier();
-                if (s + C::NB < S) issue(s + C::NB);
-                read(next, s + 1);
-            }
-            multiply(now, Half<1>{});
+            __builtin_amdgcn_sched_barrier(0);
         };
-        for (int s = 0; s < S; s += 2) {
-            stage(s, ops[0], ops[1]);
-            if (s + 1 < S) stage(s + 1, ops[1], ops[0]);
+        // (At the row's end the wait, the preparation and the reads of a stage that does not
+        // exist are harmless: old bytes of this workgroup's LDS that nothing uses.)
+        auto stage = [&](int s, auto phase) {
+            constexpr int PH = decltype(phase)::PH;
+            const int after = at + 1 == C::NB ? 0 : at + 1;
+            if constexpr (BY_ROWS)
+                read_w(wt[1], at, 1);
+            else
+                read_t(tk[1], at, 1);
+            if (s + C::NB <= S)
+                wait_vm<C::behind(PH)>();
+            else
+                wait_vm<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(phase, Part<0, 0>{});
+            if constexpr (PH == 3) prepare_scales((s + 1) / 4);
+            zero_groups(out[(PH + 1) % 4], after);
+            multiply(phase, Part<0, 1>{});
+            stage_barrier();
+            multiply(phase, Part<1, 0>{});
+            if (s + C::NB < S) {
+                if constexpr ((PH + C::NB) % 4 == 0) issue_scales((s + C::NB) / 4);
+                issue(s + C::NB, at, s + C::NB == S - 1);
+            }
+            read_w(wt[BY_ROWS ? 0 : (PH + 1) & 1], after, 0);
+            read_t(tk[BY_ROWS ? (PH + 1) & 1 : 0], after, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(phase, Part<1, 1>{});
+            if constexpr (PH == 3) read_s();
+            at = after;
+        };
+        for (int s = 0;; s += 4) {
+            stage(s, Phase<0>{});
+            if (s + 1 >= S) break;
+            stage(s + 1, Phase<1>{});
+            if (s + 2 >= S) break;
+            stage(s + 2, Phase<2>{});
+            if (s + 3 >= S) break;
+            stage(s + 3, Phase<3>{});
+            if (s + 4 >= S) break;
         }
 
         // ---- out
+        int out_lane = lane;
+        __asm__ volatile("" : "+v"(out_lane));
+        const int ro = out_lane & 15, qo = out_lane >> 4;
+        if constexpr (C::MODE == GLU) {
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            const int t = (wc * C::FN + j) * 16 + r;
-            const bool live = t < n_tok;
-            if constexpr (C::MODE == GLU) {
+            for (int j = 0; j < C::FN; ++j) {
+                const int t = (wc * C::FN + j) * 16 + ro;
+                const bool live = t < n_tok;
 #pragma unroll
                 for (int i = 0; i < C::FM / 2; i += 2) {
                     const int row = m0 + wr * C::FM * 8 + 16 * i;
@@ -378,11 +455,19 @@ __global__ __launch_bounds__(C::THREADS) void mx_tile_kernel(MmArgs a) {
                     else
                         store_h<K3G_MXFP8>(a, p + t, row / kGroup, h[0], h[1], on);
                 }
-            } else if (live) {
-#pragma unroll
-                for (int i = 0; i < C::FM; ++i)
-                    store4(a, p + t, m0 + (wr * C::FM + i) * 16 + 4 * q, acc[i][j]);
             }
+        }
+        if constexpr (C::MODE != GLU) {
+            const int row = m0 + wr * C::FM * 16 + 4 * qo, t0 = wc * C::FN * 16 + ro;
+            with_store(a, [&](auto store) {
+                int64_t at = (int64_t)(p + t0) * a.ys + row;
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j, at += 16 * a.ys)
+                    if (t0 + 16 * j < n_tok) {
+#pragma unroll
+                        for (int i = 0; i < C::FM; ++i) store(at + 16 * i, a.rows - row - 16 * i, acc[i][j]);
+                    }
+            });
         }
         __syncthreads();  // the next item's loads come after everyone's last reads
     }
@@ -405,24 +490,35 @@ int launch(const MmArgs &a, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
-template <int AF, int MODE>
+#ifndef K3G_TILE_BIG
+#define K3G_TILE_BIG 2, 4, 8, 4, 4
+#endif
+#ifndef K3G_TILE_MID
+#define K3G_TILE_MID 2, 2, 4, 4, 3
+#endif
+#ifndef K3G_TILE_LOW
+#define K3G_TILE_LOW 2, 2, 4, 2, 3
+#endif
+
+template <int AF, int MODE, bool ODD>
 int launch_mode(const MmArgs &a, hipStream_t st) {
-    if (MODE == DENSE ? a.T <= 64 : a.T <= 16 * a.E) return launch<AF, Tile<AF, MODE, 4, 1, 4, 4, 3>>(a, st);
-    if constexpr (AF == K3G_MXFP4 && MODE == DENSE) {
-        if ((int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, 2, 2, 8, 8, 4>>(a, st);
+    if (MODE == DENSE ? a.T <= 64 : a.T <= 32 * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
+    if constexpr (AF == K3G_MXFP4) {
+        if (MODE == DENSE && (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
     }
-    return launch<AF, Tile<AF, MODE, 2, 2, 4, 4, AF == K3G_MXFP4 ? 3 : 2>>(a, st);
+    return launch<AF, Tile<AF, MODE, K3G_TILE_MID, ODD>>(a, st);
 }
 
-template <int AF>
+template <int AF, bool ODD>
 int launch_af(const MmArgs &a, int mode, hipStream_t st) {
-    return mode == DENSE     ? launch_mode<AF, DENSE>(a, st)
-           : mode == GROUPED ? launch_mode<AF, GROUPED>(a, st)
-                             : launch_mode<AF, GLU>(a, st);
+    return mode == DENSE     ? launch_mode<AF, DENSE, ODD>(a, st)
+           : mode == GROUPED ? launch_mode<AF, GROUPED, ODD>(a, st)
+                             : launch_mode<AF, GLU, ODD>(a, st);
 }
 
 int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st) {
-    return af == K3G_MXFP4 ? launch_af<K3G_MXFP4>(a, mode, st) : launch_af<K3G_MXFP8>(a, mode, st);
+    if (a.odd) return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, true>(a, mode, st) : launch_af<K3G_MXFP8, true>(a, mode, st);
+    return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, false>(a, mode, st) : launch_af<K3G_MXFP8, false>(a, mode, st);
 }
 
 }  // namespace k3g
