@@ -49,6 +49,7 @@ struct Tile {
     static constexpr int TABLE = SCALES_AT + SCALES;  // then the grouped form's table
     static constexpr int lds(int E) { return TABLE + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
     static constexpr int WGS = lds(900) <= 81920 ? 2 : 1;
+    static constexpr int WAVES = THREADS / 256 * WGS < 2 ? 1 : 2;  // wavefronts per SIMD that the registers allow for
     // loads in flight behind stage s+1 (s % 4 = ph): stages s+2 .. s+NB-1
     static constexpr int behind(int ph) {
         int n = (NB - 2) * V;
@@ -100,11 +101,15 @@ __device__ inline void mul_column(const uint4 *w, const uint4 *t, const uint32_t
                                  acc[I0 + I][J], sw[I0 + I], st)),
      ...);
 }
-// Token tiles J0 + J... with the weights' tiles I0 .. I0+NI-1 (w, t: those tiles).
+// Token tiles J0 + J... with the weights' tiles I0 .. I0+NI-1 (w, t: those tiles);
+// the wavefront has tokens in its first nf tiles only (uniform; a dense product's
+// tiles are nearly all full, and there the branches cost 5%).
 template <int AF, class C, int PH, int I0, int NI, int J0, int... J>
 __device__ inline void mul_tiles(const uint4 *w, const uint4 (*t)[C::AB / 64], const uint32_t *sw, const uint32_t *st,
-                                 float4_t (*acc)[C::FN], Seq<J...>) {
-    (mul_column<AF, C, PH, J0 + J, I0>(w, t[J], sw, st[J0 + J], acc, typename MakeSeq<NI>::type{}), ...);
+                                 float4_t (*acc)[C::FN], int nf, Seq<J...>) {
+    ((C::MODE == DENSE || J0 + J < nf ? mul_column<AF, C, PH, J0 + J, I0>(w, t[J], sw, st[J0 + J], acc, typename MakeSeq<NI>::type{})
+                  : void()),
+     ...);
 }
 
 template <int H_, int Q_>
@@ -117,7 +122,7 @@ struct Phase {
 };
 
 template <int AF, class C>
-__global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile_kernel(MmArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a) {
     extern __shared__ __align__(1024) uint8_t lds[];
     int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -166,25 +171,12 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
     const int xcd = blockIdx.x % 8, step = gridDim.x / 8;
     const int64_t last = n_items * (xcd + 1) / 8;
     for (int64_t item = n_items * xcd / 8 + blockIdx.x / 8; item < last; item += step) {
-        int tile, rb;
-        if constexpr (C::MODE == DENSE) {
-            // token tiles in groups of four, row block by row block: the
-            // workgroups of an XCD that run together read 4 token tiles and a
-            // quarter as many row blocks as there are of them
-            const int64_t group = item / (4 * n_rb), in_group = item - group * 4 * n_rb;
-            const int wide = min(4, n_tiles - (int)group * 4);
-            rb = (int)in_group / wide;
-            tile = (int)group * 4 + (int)in_group % wide;
-        } else {
-            tile = (int)(item / n_rb);
-            rb = (int)(item % n_rb);
-        }
-        const int m0 = rb * C::OUT;
-        int e = 0, p, end;
-        if constexpr (C::MODE == DENSE) {
-            p = tile * C::BN;
-            end = a.T;
-        } else {
+        // the item's expert (its first tile, and how many), then row blocks by
+        // groups of four token tiles: the workgroups of an XCD that run together
+        // read 4 token tiles and a quarter as many row blocks as there are of them
+        int e = 0, t0 = 0, nt = n_tiles;
+        if constexpr (C::MODE != DENSE) {
+            const int tile = (int)(item / n_rb);
             int lo = 0, hi = a.E;  // the last expert whose first tile is at most this one
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
@@ -194,10 +186,19 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
                     hi = mid;
             }
             e = __builtin_amdgcn_readfirstlane(lo);
-            p = max(__builtin_amdgcn_readfirstlane(a.offsets[e]), 0) +
-                (tile - __builtin_amdgcn_readfirstlane(table[e])) * C::BN;
+            t0 = __builtin_amdgcn_readfirstlane(table[e]);
+            nt = __builtin_amdgcn_readfirstlane(table[e + 1]) - t0;
+        }
+        const int64_t in_expert = item - (int64_t)t0 * n_rb;
+        const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
+        if (wide < 1) continue;  // a table that does not ascend
+        const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
+        const int m0 = in_group / wide * C::OUT;
+        int p = (group * 4 + in_group % wide) * C::BN, end = a.T;
+        if constexpr (C::MODE != DENSE) {
+            p += max(__builtin_amdgcn_readfirstlane(a.offsets[e]), 0);
             end = min(__builtin_amdgcn_readfirstlane(a.offsets[e + 1]), a.T);
-            if (p < 0 || p >= end) continue;
+            if (p < 0 || p >= end || m0 >= a.rows) continue;
         }
         const int n_tok = min(C::BN, end - p);
 
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
         uint32_t sw[C::FM], st[C::FN];
         const int r = lane & 15, q = lane >> 4;
         const int w_at = (wr * C::FM * 16 + r) * 64 + 16 * (q ^ ((r >> 1) & 3));
-        const int a_at = C::BM * 64 + (wc * C::FN * 16 + r) * C::AB +
+        const int a_at = C::BM * 64 + (wc * 16 + r) * C::AB +
                          16 * (AF == K3G_MXFP4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7));
         auto read_w = [&](uint4 *o, int buffer, int half) {
 #pragma unroll
@@ -347,16 +348,19 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
             for (int f = 0; f < HN; ++f)
 #pragma unroll
                 for (int k = 0; k < C::AB / 64; ++k)
-                    o[f][k] = *(const uint4 *)(lds + buffer * C::STAGE + (a_at ^ (64 * k)) + (half * HN + f) * 16 * C::AB);
+                    o[f][k] = *(const uint4 *)(lds + buffer * C::STAGE + (a_at ^ (64 * k)) + (half * HN + f) * C::WC * 16 * C::AB);
         };
         auto read_s = [&] {
             const uint8_t *sc = lds + C::SCALES_AT + 16 * r + 4 * q;
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) sw[i] = *(const uint32_t *)(sc + (wr * C::FM + i) * 256);
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) st[j] = *(const uint32_t *)(sc + C::BM * 16 + (wc * C::FN + j) * 256);
+            for (int j = 0; j < C::FN; ++j) st[j] = *(const uint32_t *)(sc + C::BM * 16 + (wc + C::WC * j) * 256);
         };
 
+        // A tile's token tiles go round the wavefronts: with few tokens each has its share of
+        // them, and the empty ones are left out.
+        const int nf = ((n_tok + 15) / 16 - wc + C::WC - 1) / C::WC;
         float4_t acc[C::FM][C::FN];
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
@@ -381,10 +385,11 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
             constexpr int PH = decltype(phase)::PH, H = decltype(part)::H, Q = decltype(part)::Q;
             if constexpr (BY_ROWS) {
                 constexpr int N0 = C::FN / 2, J0 = Q * N0, N = Q ? C::FN - N0 : N0;
-                mul_tiles<AF, C, PH, H * HM, HM, J0>(wt[H], tk[PH & 1] + J0, sw, st, acc, typename MakeSeq<N>::type{});
+                mul_tiles<AF, C, PH, H * HM, HM, J0>(wt[H], tk[PH & 1] + J0, sw, st, acc, nf,
+                                                         typename MakeSeq<N>::type{});
             } else {
                 constexpr int N0 = (HN + 1) / 2, J0 = Q * N0, N = Q ? HN - N0 : N0;
-                mul_tiles<AF, C, PH, 0, HM, H * HN + J0>(wt[PH & 1], tk[H] + J0, sw, st, acc,
+                mul_tiles<AF, C, PH, 0, HM, H * HN + J0>(wt[PH & 1], tk[H] + J0, sw, st, acc, nf,
                                                          typename MakeSeq<N>::type{});
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -438,7 +443,8 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
         if constexpr (C::MODE == GLU) {
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
-                const int t = (wc * C::FN + j) * 16 + ro;
+                if (j >= nf) break;
+                const int t = (wc + C::WC * j) * 16 + ro;
                 const bool live = t < n_tok;
 #pragma unroll
                 for (int i = 0; i < C::FM / 2; i += 2) {
@@ -458,12 +464,12 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS / 256 * C::WGS) void mx_tile
             }
         }
         if constexpr (C::MODE != GLU) {
-            const int row = m0 + wr * C::FM * 16 + 4 * qo, t0 = wc * C::FN * 16 + ro;
+            const int row = m0 + wr * C::FM * 16 + 4 * qo, t0 = wc * 16 + ro;
             with_store(a, [&](auto store) {
                 int64_t at = (int64_t)(p + t0) * a.ys + row;
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j, at += 16 * a.ys)
-                    if (t0 + 16 * j < n_tok) {
+                for (int j = 0; j < C::FN; ++j, at += C::WC * 16 * a.ys)
+                    if (t0 + C::WC * 16 * j < n_tok) {
 #pragma unroll
                         for (int i = 0; i < C::FM; ++i) store(at + 16 * i, a.rows - row - 16 * i, acc[i][j]);
                     }
@@ -494,18 +500,25 @@ int launch(const MmArgs &a, hipStream_t st) {
 #define K3G_TILE_BIG 2, 4, 8, 4, 4
 #endif
 #ifndef K3G_TILE_MID
-#define K3G_TILE_MID 2, 2, 4, 4, 3
+#define K3G_TILE_MID 4, 2, 4, 4, 4
 #endif
 #ifndef K3G_TILE_LOW
 #define K3G_TILE_LOW 2, 2, 4, 2, 3
 #endif
 
+#ifndef K3G_TILE_MID8
+#define K3G_TILE_MID8 2, 4, 8, 2, 3
+#endif
+#ifndef K3G_LOW_PER
+#define K3G_LOW_PER 32
+#endif
 template <int AF, int MODE, bool ODD>
 int launch_mode(const MmArgs &a, hipStream_t st) {
-    if (MODE == DENSE ? a.T <= 64 : a.T <= 32 * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
+    if (MODE == DENSE ? a.T <= 64 : a.T <= K3G_LOW_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
     if constexpr (AF == K3G_MXFP4) {
         if (MODE == DENSE && (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
     }
+    if constexpr (AF == K3G_MXFP8) return launch<AF, Tile<AF, MODE, K3G_TILE_MID8, ODD>>(a, st);
     return launch<AF, Tile<AF, MODE, K3G_TILE_MID, ODD>>(a, st);
 }
 
