@@ -20,7 +20,7 @@ struct MmArgs {
     int rows;     // outputs
     int in, G;    // entries, groups of a row
     int E, top_k;
-    int y_type, y_vec;  // y_vec: four outputs are one aligned store
+    int y_type, y_vec;  // y_vec: eight outputs lie at 16-byte addresses, and rows are a multiple of 8
     int h_format;
     int odd;  // some row's scale bytes lie off 16-byte addresses, or its groups end inside sixteen
 };
@@ -72,27 +72,34 @@ __device__ inline uint4 keep4(const uint4 &v, bool keep) {
 
 enum { DENSE = 0, GROUPED = 1, GLU = 2 };
 
-// Four consecutive outputs of one token, at element `at` of y; the first `n` of
-// them exist (n below 4 only without VEC: there, rows are a multiple of 4).
+// Weight rows go to the operand tiles in pairs: of 32 consecutive rows, lane
+// r + 16q of the pair's tile k takes row 8 (r/4) + r%4 + 4k, so that a lane's
+// four results of tile 0 and four of tile 1 are the eight consecutive rows
+// 8q .. 8q+7, one wide store.
+__device__ inline int pair_row(int r, int k) { return 8 * (r >> 2) + (r & 3) + 4 * k; }
+
+// Eight consecutive outputs of one token, at element `at` of y; the first `n`
+// exist (VEC: all or none).
 template <int TYPE, bool VEC>
-__device__ inline void store4(void *y, int64_t at, int n, const float4_t &v) {
+__device__ inline void store8(void *y, int64_t at, int n, const float4_t &lo, const float4_t &hi) {
     typedef typename Elem<TYPE>::T T;
     T *p = (T *)y + at;
     if (n <= 0) return;
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     if constexpr (VEC) {
-        store_n<TYPE, 4>((T *)__builtin_assume_aligned(p, 4 * sizeof(T)), (const float *)&v);
+        store_n<TYPE, 8>((T *)__builtin_assume_aligned(p, 16), v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = Elem<TYPE>::store(v[i]);
     }
 }
 
-// f(store) with store = store4 for y's type and alignment (uniform).
+// f(store) with store = store8 for y's type and alignment (uniform).
 template <class F>
 __device__ inline void with_store(const MmArgs &a, F f) {
 #define K3G_STORE(TYPE, VEC) \
-    f([&](int64_t at, int n, const float4_t &v) { store4<TYPE, VEC>(a.y, at, n, v); })
+    f([&](int64_t at, int n, const float4_t &lo, const float4_t &hi) { store8<TYPE, VEC>(a.y, at, n, lo, hi); })
     if (a.y_vec) {
         if (a.y_type == K3G_F32)
             K3G_STORE(K3G_F32, true);
@@ -112,17 +119,17 @@ __device__ inline void with_store(const MmArgs &a, F f) {
 }
 
 // A 32-group of h of one token, spread over the four lanes r + 16q: lane q
-// holds entries 4q .. 4q+3 (h0) and 16 + 4q .. (h1). All lanes of the wavefront
+// holds entries 8q .. 8q+3 (lo) and 8q+4 .. (hi). All lanes of the wavefront
 // take part; `live` ones store.
 template <int FMT>
-__device__ inline void store_h(const MmArgs &a, int64_t token, int group, const float4_t &h0, const float4_t &h1,
+__device__ inline void store_h(const MmArgs &a, int64_t token, int group, const float4_t &lo, const float4_t &hi,
                                bool live) {
     const int q = (threadIdx.x & (kWave - 1)) >> 4;
     float v[8];  // (a bit cast of a vector's element would read element 0 whatever the index)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = h0[i];
-        v[4 + i] = h1[i];
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
     }
     uint32_t m = 0;
 #pragma unroll
@@ -137,15 +144,10 @@ __device__ inline void store_h(const MmArgs &a, int64_t token, int group, const 
     mx_codes8<FMT>(v, pow2(e), w);
     if (!live) return;
     const int64_t G = a.rows / kGroup, at = token * G + group;
-    if constexpr (FMT == K3G_MXFP4) {
-        uint8_t *c = a.h_codes + at * 16 + 2 * q;
-        *(uint16_t *)c = (uint16_t)w[0];
-        *(uint16_t *)(c + 8) = (uint16_t)(w[0] >> 16);
-    } else {
-        uint8_t *c = a.h_codes + at * 32 + 4 * q;
-        *(uint32_t *)c = w[0];
-        *(uint32_t *)(c + 16) = w[1];
-    }
+    if constexpr (FMT == K3G_MXFP4)
+        *(uint32_t *)(a.h_codes + at * 16 + 4 * q) = w[0];
+    else
+        *(uint2 *)(a.h_codes + at * 32 + 8 * q) = make_uint2(w[0], w[1]);
     if (q == 0) a.h_scales[at] = fine ? (uint8_t)(e + 127) : (uint8_t)255;
 }
 

@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
         const uint8_t *wc[TILES], *wsc[TILES];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int64_t row = min(row0 + 16 * (t & 1) + r, a.rows - 1);
+            const int64_t row = min(row0 + pair_row(r, t & 1), a.rows - 1);
             wc[t] = a.w[t >> 1] + e * a.stride + row * w_pitch;
             wsc[t] = a.ws[t >> 1] + e * a.stride + row * a.G;
         }
@@ -106,10 +106,10 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
                 else
                     store_h<K3G_MXFP8>(a, p + r, row0 / kGroup, h[0], h[1], live);
             }
-        } else if (wave < 2) {
-            const float4_t s = sum(wave);
-            const int row = row0 + 16 * wave + 4 * q;
-            if (r < n_tok) with_store(a, [&](auto store) { store((p + r) * a.ys + row, a.rows - row, s); });
+        } else if (wave == 0) {
+            const float4_t lo = sum(0), hi = sum(1);
+            const int row = row0 + 8 * q;
+            if (r < n_tok) with_store(a, [&](auto store) { store((p + r) * a.ys + row, a.rows - row, lo, hi); });
         }
         __syncthreads();  // part is read before the next tile writes it
     }
@@ -172,7 +172,7 @@ int groups_ok(const k3g_mx *a, const int32_t *offsets, const int32_t *perm, int 
 }
 
 int y_vec(const void *y, int type, int64_t stride, int rows) {
-    return mx_aligned(y, 4 * type_size(type)) && stride % 4 == 0 && rows % 4 == 0;
+    return mx_aligned(y, 16) && stride * (int64_t)type_size(type) % 16 == 0 && rows % 8 == 0;
 }
 
 // Whether some row's scale bytes lie off 16-byte addresses, or end inside sixteen.

@@ -4,9 +4,9 @@
 //
 // A stage holds 64 bytes of each weight row and 64 (e2m1) or 128 (e4m3) of each
 // token, written by LDS DMA: four (eight) consecutive lanes take one row's
-// contiguous bytes, 16-byte chunk c of row i at place c ^ (i/2 % 4) (c ^ i % 8),
-// so that the operand reads (16 bytes of 16 rows a quarter wavefront) meet no
-// bank twice. Scales come for four stages at a time, 16 bytes a row: one lane a
+// contiguous bytes, each 16-byte chunk at a place that depends on the row, so
+// that the operand reads (16 bytes of 16 rows a quarter wavefront) meet no bank
+// twice. Scales come for four stages at a time, 16 bytes a row: one lane a
 // row, whatever the width of the request, so a request a stage would cost the
 // address unit as much as the data. The wavefront that loaded a row turns its
 // bytes into operand order (for each group of a step one dword, a byte for each
@@ -46,7 +46,8 @@ struct Tile {
     static constexpr int STAGE = BM * 64 + BN * AB, RAW_W = kWave * (ODD ? 20 : 16), RAW = NW * RAW_W;
     static constexpr int SCALES = (BM + BN) * 16;
     static constexpr int RAW_AT = NB * STAGE, SCALES_AT = RAW_AT + RAW;
-    static constexpr int TABLE = SCALES_AT + SCALES;  // then the grouped form's table
+    static constexpr int PERM_AT = SCALES_AT + SCALES;  // grouped: the next tile's source rows, and the table
+    static constexpr int TABLE = PERM_AT + (MODE == DENSE ? 0 : NW * kWave * 4);
     static constexpr int lds(int E) { return TABLE + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
     static constexpr int WGS = lds(900) <= 81920 ? 2 : 1;
     static constexpr int WAVES = THREADS / 256 * WGS < 2 ? 1 : 2;  // wavefronts per SIMD that the registers allow for
@@ -58,6 +59,11 @@ struct Tile {
         return n;
     }
 };
+
+// Where chunk c of weight row i lies: c ^ w_swz(i). The rows of an operand tile
+// are four of every eight (pair_row), and any eight lanes' rows meet each of the
+// eight 16-byte places of 128 bytes once.
+__device__ inline int w_swz(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
 
 __device__ inline void stage_barrier() {
     __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
@@ -124,8 +130,7 @@ struct Phase {
 template <int AF, class C>
 __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a) {
     extern __shared__ __align__(1024) uint8_t lds[];
-    int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wr = wave / C::WC, wc = wave % C::WC;
     const uint32_t lds0 = lds_addr(lds);
     const int n_rb = (a.rows + C::OUT - 1) / C::OUT;
@@ -165,237 +170,265 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     }
 
     // Workgroup b runs on XCD b % 8; each XCD takes a contiguous eighth of the
-    // items, row blocks of one token tile after one another, so that its L2
-    // serves the tokens of a tile to all of them.
+    // items: an expert after another, and in it row blocks by groups of four
+    // token tiles, so the workgroups of an XCD that run together read 4 token
+    // tiles and a quarter as many row blocks as there are of them.
     const int64_t n_items = (int64_t)n_tiles * n_rb;
     const int xcd = blockIdx.x % 8, step = gridDim.x / 8;
     const int64_t last = n_items * (xcd + 1) / 8;
-    for (int64_t item = n_items * xcd / 8 + blockIdx.x / 8; item < last; item += step) {
-        // the item's expert (its first tile, and how many), then row blocks by
-        // groups of four token tiles: the workgroups of an XCD that run together
-        // read 4 token tiles and a quarter as many row blocks as there are of them
-        int e = 0, t0 = 0, nt = n_tiles;
-        if constexpr (C::MODE != DENSE) {
-            const int tile = (int)(item / n_rb);
-            int lo = 0, hi = a.E;  // the last expert whose first tile is at most this one
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (table[mid] <= tile)
-                    lo = mid;
-                else
-                    hi = mid;
+    struct Item {
+        int e, p, n_tok, m0;
+    };
+    int near = 0;  // an expert at or before the next item's
+    // the first item from `item` on that has tokens (all have, in an ascending table); its successor in `item`
+    auto next_item = [&](int64_t &item, Item &o) {
+        for (; item < last; item += step) {
+            int t0 = 0, nt = n_tiles;
+            o.e = 0;
+            if constexpr (C::MODE != DENSE) {
+                const int tile = (int)(item / n_rb);
+                // experts after `near` whose first tile is at most this one, 64 at a time
+                for (;;) {
+                    const int i = near + 1 + lane;
+                    const int n = __popcll(__ballot(i < a.E && table[min(i, a.E)] <= tile));
+                    near += n;
+                    if (n < kWave) break;
+                }
+                near = __builtin_amdgcn_readfirstlane(near);
+                o.e = near;
+                t0 = __builtin_amdgcn_readfirstlane(table[near]);
+                nt = __builtin_amdgcn_readfirstlane(table[near + 1]) - t0;
             }
-            e = __builtin_amdgcn_readfirstlane(lo);
-            t0 = __builtin_amdgcn_readfirstlane(table[e]);
-            nt = __builtin_amdgcn_readfirstlane(table[e + 1]) - t0;
+            const int64_t in_expert = item - (int64_t)t0 * n_rb;
+            const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
+            if (wide < 1) continue;
+            const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
+            o.m0 = in_group / wide * C::OUT;
+            o.p = (group * 4 + in_group % wide) * C::BN;
+            int end = a.T;
+            if constexpr (C::MODE != DENSE) {
+                o.p += max(__builtin_amdgcn_readfirstlane(a.offsets[o.e]), 0);
+                end = min(__builtin_amdgcn_readfirstlane(a.offsets[o.e + 1]), a.T);
+            }
+            o.n_tok = min(C::BN, end - o.p);
+            if (o.p < 0 || o.n_tok < 1 || o.m0 >= a.rows) continue;
+            item += step;
+            return true;
         }
-        const int64_t in_expert = item - (int64_t)t0 * n_rb;
-        const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
-        if (wide < 1) continue;  // a table that does not ascend
-        const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
-        const int m0 = in_group / wide * C::OUT;
-        int p = (group * 4 + in_group % wide) * C::BN, end = a.T;
-        if constexpr (C::MODE != DENSE) {
-            p += max(__builtin_amdgcn_readfirstlane(a.offsets[e]), 0);
-            end = min(__builtin_amdgcn_readfirstlane(a.offsets[e + 1]), a.T);
-            if (p < 0 || p >= end || m0 >= a.rows) continue;
-        }
-        const int n_tok = min(C::BN, end - p);
+        return false;
+    };
 
-        // what depends on the lane is computed again for each item, and again for the way out:
-        // kept across the products it would not fit the registers
-        __asm__ volatile("" : "+v"(lane));
-        // ---- what this wavefront loads: MW weight rows from row MW * wave, MA tokens from MA * wave
-        const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
-        // row i of the tile's weights: tensor and row past m0
-        auto w_tensor = [&](int i) { return C::MODE == GLU ? (i / (C::FM * 8)) & 1 : 0; };
-        auto w_row = [&](int i) {
+    // ---- what this wavefront loads: MW weight rows from row MW * wave, MA tokens from MA * wave
+    const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
+    const int S = (a.G + 3) / 4, Gt = a.G - 4 * (S - 1);  // stages, groups of the last
+    const bool is_w = lane < C::MW, has_row = lane < C::MW + C::MA;
+    const int iw = wave * C::MW + min(lane, C::MW - 1), ia_own = min(max(lane - C::MW, 0), C::MA - 1);
+    const int ia = wave * C::MA + ia_own;
+    const int cw = (lane & 3) ^ w_swz(lane >> 2);                     // the chunk this lane moves, of row lane / 4
+    const int ca = AF == K3G_MXFP4 ? (lane & 3) ^ ((lane >> 3) & 3)  // ... of a token
+                                   : (lane & 7) ^ (lane >> 3);
+    auto w_tensor = [&](int i) { return C::MODE == GLU ? (i / (C::FM * 8)) & 1 : 0; };  // of row i of the tile
+    // the addresses that the loads are issued from: those of the item being loaded
+    uint32_t vw[C::DW], va[C::DA];
+    const uint8_t *bw[C::DW], *ba;
+    uint64_t s_addr;  // of the row whose scales this lane loads and prepares: a weight row, from lane MW on a token
+    // the tile's entries of perm, fetched ahead (each wavefront its own tokens')
+    int32_t *perm = (int32_t *)(lds + C::PERM_AT) + wave * kWave;
+    auto fetch_perm = [&](const Item &o) {
+        if (C::MODE != DENSE && a.perm && lane < C::MA)
+            dma4_at(a.perm + o.p + min(wave * C::MA + lane, o.n_tok - 1), lds0 + C::PERM_AT + wave * kWave * 4);
+    };
+    auto address = [&](const Item &o) {
+        auto w_row = [&](int i) {  // row past m0 of row i of the tile
             const int row = C::MODE == GLU ? i / (C::FM * 16) * (C::FM * 8) + i % (C::FM * 8) : i;
-            return min(row, a.rows - 1 - m0);
+            return min(row, a.rows - 1 - o.m0);
         };
-        const int cw = (lane & 3) ^ ((lane >> 3) & 3);  // the chunk this lane moves, of row lane / 4
-        const int ca = AF == K3G_MXFP4 ? cw : (lane & 7) ^ (lane >> 3);  // ... of row lane / 8
-        uint32_t vw[C::DW], va[C::DA];
-        const uint8_t *bw[C::DW];
-        const uint8_t *ba = a.perm ? a.a_codes : a.a_codes + (int64_t)p * a_pitch;
-        auto a_row = [&](int i) {  // row of the activations past ba
-            const int t = min(i, n_tok - 1);
-            return a.perm ? source_row(a, p + t) : t;
+        const bool gather = C::MODE != DENSE && a.perm;
+        auto a_row = [&](int own) {  // row past ba of this wavefront's token `own`
+            if (!gather) return min(wave * C::MA + own, o.n_tok - 1);
+            return min(max(perm[own] / a.top_k, 0), a.a_rows - 1);
         };
+        ba = gather ? a.a_codes : a.a_codes + (int64_t)o.p * a_pitch;
 #pragma unroll
         for (int d = 0; d < C::DW; ++d) {
             const int i = wave * C::MW + 16 * d;
-            bw[d] = a.w[w_tensor(i)] + e * a.stride + (int64_t)m0 * w_pitch;
+            bw[d] = a.w[w_tensor(i)] + o.e * a.stride + (int64_t)o.m0 * w_pitch;
             vw[d] = (uint32_t)w_row(i + lane / 4) * w_pitch + 16 * cw;
         }
         constexpr int RA = 1024 / C::AB;  // tokens of one DMA instruction
 #pragma unroll
+        for (int d = 0; d < C::DA; ++d) va[d] = (uint32_t)a_row(RA * d + lane / (64 / RA)) * a_pitch + 16 * ca;
+        s_addr = is_w ? (uint64_t)(a.ws[w_tensor(iw)] + o.e * a.stride) + (uint64_t)(o.m0 + w_row(iw)) * a.G
+                      : (uint64_t)a.a_scales + ((uint64_t)(gather ? 0 : o.p) + (uint64_t)a_row(ia_own)) * a.G;
+    };
+    auto issue = [&](int s, int buffer) {
+        const uint32_t buf = lds0 + (uint32_t)buffer * C::STAGE;
+        // past the row's end the last whole chunk is read again (its place is zeroed later)
+        const bool tail = s == S - 1;
+        const uint32_t backw = tail ? 16u * (uint32_t)max(cw - (Gt - 1), 0) : 0u;
+        const uint32_t backa = tail ? 16u * (uint32_t)max(ca - (AF == K3G_MXFP4 ? Gt - 1 : 2 * Gt - 1), 0) : 0u;
+#pragma unroll
+        for (int d = 0; d < C::DW; ++d)
+            dma16(bw[d] + 64 * (int64_t)s, vw[d] - backw, buf + (wave * C::MW + 16 * d) * 64);
+#pragma unroll
         for (int d = 0; d < C::DA; ++d)
-            va[d] = (uint32_t)a_row(wave * C::MA + RA * d + lane / (64 / RA)) * a_pitch + 16 * ca;
-        // the row whose scales this lane loads and prepares: a weight row, from lane MW on a token
-        const bool is_w = lane < C::MW, has_row = lane < C::MW + C::MA;
-        const int iw = wave * C::MW + min(lane, C::MW - 1);
-        const int ia = wave * C::MA + min(max(lane - C::MW, 0), C::MA - 1);
-        const uint64_t s_addr =
-            is_w ? (uint64_t)(a.ws[w_tensor(iw)] + e * a.stride) + (uint64_t)(m0 + w_row(iw)) * a.G
-                 : (uint64_t)a.a_scales + ((uint64_t)(a.perm ? 0 : p) + (uint64_t)a_row(ia)) * a.G;
-        const int S = (a.G + 3) / 4, Gt = a.G - 4 * (S - 1);  // stages, groups of the last
-
-        auto issue = [&](int s, int buffer, bool tail) {
-            const uint32_t buf = lds0 + (uint32_t)buffer * C::STAGE;
-            // past the row's end the last whole chunk is read again (its place is zeroed later)
-            const uint32_t backw = tail ? 16u * (uint32_t)max(cw - (Gt - 1), 0) : 0u;
-            const uint32_t backa =
-                tail ? 16u * (uint32_t)max(ca - (AF == K3G_MXFP4 ? Gt - 1 : 2 * Gt - 1), 0) : 0u;
+            dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + wave * C::MA * C::AB + 1024 * d);
+    };
+    const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
+    auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
+        if (!has_row) return;         // (lane 0 always has one)
+        const uint64_t at = s_addr + 16 * (uint64_t)u;
+        if constexpr (!C::ODD) {
+            dma16_at((const void *)at, raw);
+        } else {
+            // the aligned dwords that hold the bytes; past the row's last byte, the one that holds it
+            const uint64_t end = (s_addr + a.G - 1) & ~3ull;
 #pragma unroll
-            for (int d = 0; d < C::DW; ++d)
-                dma16(bw[d] + 64 * (int64_t)s, vw[d] - backw, buf + (wave * C::MW + 16 * d) * 64);
-#pragma unroll
-            for (int d = 0; d < C::DA; ++d)
-                dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + wave * C::MA * C::AB + 1024 * d);
-        };
-        const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
-        auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
-            if (!has_row) return;         // (lane 0 always has one)
-            const uint64_t at = s_addr + 16 * (uint64_t)u;
-            if constexpr (!C::ODD) {
-                dma16_at((const void *)at, raw);
-            } else {
-                // the aligned dwords that hold the bytes; past the row's last byte, the one that holds it
-                const uint64_t last = (s_addr + a.G - 1) & ~3ull;
-#pragma unroll
-                for (int k = 0; k < 5; ++k) {
-                    const uint64_t w = (at & ~3ull) + 4 * k;
-                    dma4_at((const void *)(w < last ? w : last), raw + 256 * k);
-                }
+            for (int k = 0; k < 5; ++k) {
+                const uint64_t w = (at & ~3ull) + 4 * k;
+                dma4_at((const void *)(w < end ? w : end), raw + 256 * k);
             }
-        };
+        }
+    };
 
-        // this wavefront's rows: the scales of the stages 4u .. to operand order, and a stage's
-        // groups that add nothing (bits in `out`, a dword a stage) zeroed
-        const int s_at = C::SCALES_AT + 16 * (is_w ? iw : C::BM + ia);
-        const int d_at = is_w ? iw * 64 : C::BM * 64 + ia * C::AB;
-        const int d_swz = is_w ? (iw >> 1) & 3 : AF == K3G_MXFP4 ? (ia >> 1) & 3 : ia & 7;
-        uint32_t out[4];
-        auto prepare_scales = [&](int u) {
-            uint32_t d[4];
-            if constexpr (!C::ODD) {
-                const uint4 v = *(const uint4 *)(lds + C::RAW_AT + wave * C::RAW_W + 16 * lane);
-                d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-            } else {
-                const uint32_t *v = (const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W) + lane;
-                uint32_t lo = v[0];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t hi = v[64 * (k + 1)];
-                    d[k] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)s_addr & 3u);
-                    lo = hi;
-                    const int left = a.G - 16 * u - 4 * k;  // groups from this stage on
-                    if (left < 4) d[k] |= left > 0 ? ~0u << (8 * left) : ~0u;
-                }
-            }
+    // this wavefront's rows: the scales of the stages 4u .. to operand order, and a stage's
+    // groups that add nothing (bits in `out`, a dword a stage) zeroed
+    const int s_at = C::SCALES_AT + 16 * (is_w ? iw : C::BM + ia);
+    const int d_at = is_w ? iw * 64 : C::BM * 64 + ia * C::AB;
+    const int d_swz = is_w ? w_swz(iw) : AF == K3G_MXFP4 ? (ia >> 1) & 3 : ia & 7;
+    uint32_t out[4];
+    auto prepare_scales = [&](int u) {
+        uint32_t d[4];
+        if constexpr (!C::ODD) {
+            const uint4 v = *(const uint4 *)(lds + C::RAW_AT + wave * C::RAW_W + 16 * lane);
+            d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+        } else {
+            const uint32_t *v = (const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W) + lane;
+            uint32_t lo = v[0];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                // bytes equal to 255: b's top bit, where (b & 127) + 1 has it too; they become 127
-                const uint32_t f = ((d[k] & 0x7F7F7F7Fu) + 0x01010101u) & d[k] & 0x80808080u;
-                d[k] ^= f;
-                out[k] = has_row ? f : 0u;
+                const uint32_t hi = v[64 * (k + 1)];
+                d[k] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)s_addr & 3u);
+                lo = hi;
+                const int left = a.G - 16 * u - 4 * k;  // groups from this stage on
+                if (left < 4) d[k] |= left > 0 ? ~0u << (8 * left) : ~0u;
             }
-            // [stage][group] bytes -> [group][stage]
-            const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u);  // 0: 0,0 1,0 0,1 1,1
-            const uint32_t a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
-            const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
-            const uint32_t b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
-            const uint4 o = make_uint4(__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
-                                       __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u));
-            if (has_row) *(uint4 *)(lds + s_at) = o;
-        };
-        auto zero_groups = [&](uint32_t f, int buffer) {
-            while (__ballot(f != 0) != 0) {  // rarely entered; a group a round
-                if (f) {
-                    const int k = __builtin_ctz(f) >> 3;
-                    uint8_t *row = lds + buffer * C::STAGE + d_at;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    if (AF == K3G_MXFP4 || is_w) {
-                        *(uint4 *)(row + 16 * (k ^ d_swz)) = zero;
-                    } else {
-                        *(uint4 *)(row + 16 * ((2 * k) ^ d_swz)) = zero;
-                        *(uint4 *)(row + 16 * ((2 * k + 1) ^ d_swz)) = zero;
-                    }
-                    f &= f - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // bytes equal to 255: b's top bit, where (b & 127) + 1 has it too; they become 127
+            const uint32_t f = ((d[k] & 0x7F7F7F7Fu) + 0x01010101u) & d[k] & 0x80808080u;
+            d[k] ^= f;
+            out[k] = has_row ? f : 0u;
+        }
+        // [stage][group] bytes -> [group][stage]
+        const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+        const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u), b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+        const uint4 o = make_uint4(__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                                   __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u));
+        if (has_row) *(uint4 *)(lds + s_at) = o;
+    };
+    auto zero_groups = [&](uint32_t f, int buffer) {
+        while (__ballot(f != 0) != 0) {  // rarely entered; a group a round
+            if (f) {
+                const int k = __builtin_ctz(f) >> 3;
+                uint8_t *row = lds + buffer * C::STAGE + d_at;
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                if (AF == K3G_MXFP4 || is_w) {
+                    *(uint4 *)(row + 16 * (k ^ d_swz)) = zero;
+                } else {
+                    *(uint4 *)(row + 16 * ((2 * k) ^ d_swz)) = zero;
+                    *(uint4 *)(row + 16 * ((2 * k + 1) ^ d_swz)) = zero;
                 }
+                f &= f - 1;
             }
-        };
+        }
+    };
 
-        // Operands of a stage in two halves: by weight rows, the tokens' tiles whole and
-        // in two sets (now, next), or by tokens with the weights' whole: an e4m3
-        // tile is cut in two for the matrix cores, which is done once that way.
-        constexpr bool BY_ROWS = AF == K3G_MXFP4;
-        constexpr int HM = BY_ROWS ? C::FM / 2 : C::FM, HN = BY_ROWS ? C::FN : C::FN / 2;
-        uint4 wt[2][HM], tk[2][HN][C::AB / 64];
-        uint32_t sw[C::FM], st[C::FN];
-        const int r = lane & 15, q = lane >> 4;
-        const int w_at = (wr * C::FM * 16 + r) * 64 + 16 * (q ^ ((r >> 1) & 3));
-        const int a_at = C::BM * 64 + (wc * 16 + r) * C::AB +
-                         16 * (AF == K3G_MXFP4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7));
-        auto read_w = [&](uint4 *o, int buffer, int half) {
+    // Operands of a stage in two halves: by weight rows, the tokens' tiles whole and
+    // in two sets (now, next), or by tokens with the weights' whole: an e4m3
+    // tile is cut in two for the matrix cores, which is done once that way.
+    constexpr bool BY_ROWS = AF == K3G_MXFP4;
+    constexpr int HM = BY_ROWS ? C::FM / 2 : C::FM, HN = BY_ROWS ? C::FN : C::FN / 2;
+    uint4 wt[2][HM], tk[2][HN][C::AB / 64];
+    uint32_t sw[C::FM], st[C::FN];
+    const int r = lane & 15, q = lane >> 4;
+    const int w_at0 = (wr * C::FM * 16 + pair_row(r, 0)) * 64 + 16 * (q ^ w_swz(pair_row(r, 0)));
+    const int a_at = C::BM * 64 + (wc * 16 + r) * C::AB + 16 * (AF == K3G_MXFP4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7));
+    auto read_w = [&](uint4 *o, int buffer, int half) {
 #pragma unroll
-            for (int i = 0; i < HM; ++i)
-                o[i] = *(const uint4 *)(lds + buffer * C::STAGE + w_at + (half * HM + i) * 1024);
-        };
-        auto read_t = [&](uint4(*o)[C::AB / 64], int buffer, int half) {
+        for (int i = 0; i < HM; ++i)  // (tile 1 of a pair: 4 rows on, where the swizzle is the same)
+            o[i] = *(const uint4 *)(lds + buffer * C::STAGE + w_at0 + (half * HM + i) / 2 * 2048 + (i & 1) * 256);
+    };
+    auto read_t = [&](uint4(*o)[C::AB / 64], int buffer, int half) {
 #pragma unroll
-            for (int f = 0; f < HN; ++f)
+        for (int f = 0; f < HN; ++f)
 #pragma unroll
-                for (int k = 0; k < C::AB / 64; ++k)
-                    o[f][k] = *(const uint4 *)(lds + buffer * C::STAGE + (a_at ^ (64 * k)) + (half * HN + f) * C::WC * 16 * C::AB);
-        };
-        auto read_s = [&] {
-            const uint8_t *sc = lds + C::SCALES_AT + 16 * r + 4 * q;
+            for (int k = 0; k < C::AB / 64; ++k)
+                o[f][k] =
+                    *(const uint4 *)(lds + buffer * C::STAGE + (a_at ^ (64 * k)) + (half * HN + f) * C::WC * 16 * C::AB);
+    };
+    auto read_s = [&] {
+        const uint8_t *sw_at = lds + C::SCALES_AT + 16 * (wr * C::FM * 16 + pair_row(r, 0)) + 4 * q;
+        const uint8_t *st_at = lds + C::SCALES_AT + 16 * (C::BM + wc * 16 + r) + 4 * q;
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i) sw[i] = *(const uint32_t *)(sc + (wr * C::FM + i) * 256);
+        for (int i = 0; i < C::FM; ++i) sw[i] = *(const uint32_t *)(sw_at + i / 2 * 512 + (i & 1) * 64);
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) st[j] = *(const uint32_t *)(sc + C::BM * 16 + (wc + C::WC * j) * 256);
-        };
+        for (int j = 0; j < C::FN; ++j) st[j] = *(const uint32_t *)(st_at + j * C::WC * 256);
+    };
 
-        // A tile's token tiles go round the wavefronts: with few tokens each has its share of
-        // them, and the empty ones are left out.
-        const int nf = ((n_tok + 15) / 16 - wc + C::WC - 1) / C::WC;
-        float4_t acc[C::FM][C::FN];
+    float4_t acc[C::FM][C::FN];
+    int nf = 0;  // this wavefront's token tiles with tokens: a tile's go round the wavefronts
+    // a quarter of a stage's products: half H, part Q
+    auto multiply = [&](auto phase, auto part) {
+        constexpr int PH = decltype(phase)::PH, H = decltype(part)::H, Q = decltype(part)::Q;
+        if constexpr (BY_ROWS) {
+            constexpr int N0 = C::FN / 2, J0 = Q * N0, N = Q ? C::FN - N0 : N0;
+            mul_tiles<AF, C, PH, H * HM, HM, J0>(wt[H], tk[PH & 1] + J0, sw, st, acc, nf, typename MakeSeq<N>::type{});
+        } else {
+            constexpr int N0 = (HN + 1) / 2, J0 = Q * N0, N = Q ? HN - N0 : N0;
+            mul_tiles<AF, C, PH, 0, HM, H * HN + J0>(wt[PH & 1], tk[H] + J0, sw, st, acc, nf,
+                                                     typename MakeSeq<N>::type{});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // Rows of whole four stages run on from item to item: the last NB stages of
+    // one issue the first of the next, which land behind its way out.
+    const bool run_on = S % 4 == 0 && S >= C::NB;
+    int64_t item = n_items * xcd / 8 + blockIdx.x / 8;
+    Item now, next;
+    bool have = next_item(item, now), loaded = false;  // loaded: its first NB stages are in LDS, stage 0 prepared
+    int at = 0;                                          // the buffer of the stage being multiplied
+    while (have) {
+        const bool more = next_item(item, next), on = run_on && more;
+        if (!loaded) {
+            fetch_perm(now);
+            wait_vm<0>();
+            address(now);
+            issue_scales(0);
+            for (int s = 0; s < C::NB && s < S; ++s) issue(s, s);
+            if (S >= C::NB)
+                wait_vm<(C::NB - 1) * C::V>();
+            else
+                wait_vm<0>();
+            prepare_scales(0);
+            zero_groups(out[0], 0);
+            stage_barrier();
+            at = 0;
+        }
+        if (on) fetch_perm(next);
+        const int landed = loaded ? C::NB : 1;
+        nf = ((now.n_tok + 15) / 16 - wc + C::WC - 1) / C::WC;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-
-        issue_scales(0);
-        for (int s = 0; s < C::NB && s < S; ++s) issue(s, s, s == S - 1);
-        if (S >= C::NB)
-            wait_vm<(C::NB - 1) * C::V>();
-        else
-            wait_vm<0>();
-        prepare_scales(0);
-        zero_groups(out[0], 0);
-        stage_barrier();
         read_s();
-        read_w(wt[0], 0, 0);
-        read_t(tk[0], 0, 0);
-        int at = 0;  // the buffer of stage s
-        // a quarter of a stage's products: half H, part Q
-        auto multiply = [&](auto phase, auto part) {
-            constexpr int PH = decltype(phase)::PH, H = decltype(part)::H, Q = decltype(part)::Q;
-            if constexpr (BY_ROWS) {
-                constexpr int N0 = C::FN / 2, J0 = Q * N0, N = Q ? C::FN - N0 : N0;
-                mul_tiles<AF, C, PH, H * HM, HM, J0>(wt[H], tk[PH & 1] + J0, sw, st, acc, nf,
-                                                         typename MakeSeq<N>::type{});
-            } else {
-                constexpr int N0 = (HN + 1) / 2, J0 = Q * N0, N = Q ? HN - N0 : N0;
-                mul_tiles<AF, C, PH, 0, HM, H * HN + J0>(wt[PH & 1], tk[H] + J0, sw, st, acc, nf,
-                                                         typename MakeSeq<N>::type{});
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        // (At the row's end the wait, the preparation and the reads of a stage that does not
-        // exist are harmless: old bytes of this workgroup's LDS that nothing uses.)
+        read_w(wt[0], at, 0);
+        read_t(tk[0], at, 0);
+        // (At a row's end with nothing to follow, the wait, the preparation and the reads of a stage
+        // that does not exist are harmless: old bytes of this workgroup's LDS that nothing uses.)
         auto stage = [&](int s, auto phase) {
             constexpr int PH = decltype(phase)::PH;
             const int after = at + 1 == C::NB ? 0 : at + 1;
@@ -403,20 +436,30 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
                 read_w(wt[1], at, 1);
             else
                 read_t(tk[1], at, 1);
-            if (s + C::NB <= S)
-                wait_vm<C::behind(PH)>();
-            else
+            if (s + C::NB > S && !on)
                 wait_vm<0>();
+            else if (s + 1 >= landed)
+                wait_vm<C::behind(PH)>();
             __builtin_amdgcn_sched_barrier(0);
             multiply(phase, Part<0, 0>{});
-            if constexpr (PH == 3) prepare_scales((s + 1) / 4);
+            if constexpr (PH == 3) prepare_scales(s + 1 == S ? 0 : (s + 1) / 4);
             zero_groups(out[(PH + 1) % 4], after);
             multiply(phase, Part<0, 1>{});
             stage_barrier();
             multiply(phase, Part<1, 0>{});
-            if (s + C::NB < S) {
-                if constexpr ((PH + C::NB) % 4 == 0) issue_scales((s + C::NB) / 4);
-                issue(s + C::NB, at, s + C::NB == S - 1);
+            if (s + C::NB < S || on) {
+                int to = s + C::NB;
+                if (to >= S) {
+                    if constexpr ((PH + C::NB) % 4 == 0) {
+                        if (to == S) {
+                            if (a.perm && S < 2 * C::NB) wait_vm<0>();  // perm was fetched too late to be behind a wait
+                            address(next);
+                        }
+                    }
+                    to -= S;
+                }
+                if constexpr ((PH + C::NB) % 4 == 0) issue_scales(to / 4);
+                issue(to, at);
             }
             read_w(wt[BY_ROWS ? 0 : (PH + 1) & 1], after, 0);
             read_t(tk[BY_ROWS ? (PH + 1) & 1 : 0], after, 0);
@@ -436,7 +479,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             if (s + 4 >= S) break;
         }
 
-        // ---- out
+        // ---- out. The next item's first stages land before the stores go out: a wait for
+        // loads behind stores would wait for the stores too.
+        if (on) wait_vm<0>();
         int out_lane = lane;
         __asm__ volatile("" : "+v"(out_lane));
         const int ro = out_lane & 15, qo = out_lane >> 4;
@@ -445,37 +490,40 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             for (int j = 0; j < C::FN; ++j) {
                 if (j >= nf) break;
                 const int t = (wc + C::WC * j) * 16 + ro;
-                const bool live = t < n_tok;
+                const bool live = t < now.n_tok;
 #pragma unroll
                 for (int i = 0; i < C::FM / 2; i += 2) {
-                    const int row = m0 + wr * C::FM * 8 + 16 * i;
+                    const int row = now.m0 + wr * C::FM * 8 + 16 * i;
                     float4_t h[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             h[k][x] = situ(acc[i + k][j][x], acc[C::FM / 2 + i + k][j][x]);
-                    const bool on = live && row < a.rows;
+                    const bool in = live && row < a.rows;
                     if (a.h_format == K3G_MXFP4)
-                        store_h<K3G_MXFP4>(a, p + t, row / kGroup, h[0], h[1], on);
+                        store_h<K3G_MXFP4>(a, now.p + t, row / kGroup, h[0], h[1], in);
                     else
-                        store_h<K3G_MXFP8>(a, p + t, row / kGroup, h[0], h[1], on);
+                        store_h<K3G_MXFP8>(a, now.p + t, row / kGroup, h[0], h[1], in);
                 }
             }
-        }
-        if constexpr (C::MODE != GLU) {
-            const int row = m0 + wr * C::FM * 16 + 4 * qo, t0 = wc * 16 + ro;
+        } else {
+            const int row = now.m0 + wr * C::FM * 16 + 8 * qo, t0 = wc * 16 + ro;
             with_store(a, [&](auto store) {
-                int64_t at = (int64_t)(p + t0) * a.ys + row;
+                int64_t to = (int64_t)(now.p + t0) * a.ys + row;
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j, at += C::WC * 16 * a.ys)
-                    if (t0 + C::WC * 16 * j < n_tok) {
+                for (int j = 0; j < C::FN; ++j, to += C::WC * 16 * a.ys)
+                    if (t0 + C::WC * 16 * j < now.n_tok) {
 #pragma unroll
-                        for (int i = 0; i < C::FM; ++i) store(at + 16 * i, a.rows - row - 16 * i, acc[i][j]);
+                        for (int i = 0; i < C::FM; i += 2)
+                            store(to + 16 * i, a.rows - row - 16 * i, acc[i][j], acc[i + 1][j]);
                     }
             });
         }
-        __syncthreads();  // the next item's loads come after everyone's last reads
+        if (!on) __syncthreads();  // the next item's first loads come after everyone's last reads
+        now = next;
+        have = more;
+        loaded = on;
     }
 }
 
@@ -515,11 +563,13 @@ int launch(const MmArgs &a, hipStream_t st) {
 template <int AF, int MODE, bool ODD>
 int launch_mode(const MmArgs &a, hipStream_t st) {
     if (MODE == DENSE ? a.T <= 64 : a.T <= K3G_LOW_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
-    if constexpr (AF == K3G_MXFP4) {
-        if (MODE == DENSE && (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
+    if constexpr (AF == K3G_MXFP4 && MODE == DENSE) {
+        if ( (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
     }
-    if constexpr (AF == K3G_MXFP8) return launch<AF, Tile<AF, MODE, K3G_TILE_MID8, ODD>>(a, st);
-    return launch<AF, Tile<AF, MODE, K3G_TILE_MID, ODD>>(a, st);
+    if constexpr (AF == K3G_MXFP8)
+        return launch<AF, Tile<AF, MODE, K3G_TILE_MID8, ODD>>(a, st);
+    else
+        return launch<AF, Tile<AF, MODE, K3G_TILE_MID, ODD>>(a, st);
 }
 
 template <int AF, bool ODD>

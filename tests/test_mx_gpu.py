@@ -394,6 +394,72 @@ def test_grouped_bad_tables_stay_in_range(k3g):
     assert (b[:32] == 7.0).all() and (b[32 + P:] == 7.0).all() and np.isfinite(b).all()
 
 
+MANY = [
+    # E, latent, inter, rows a group, rows before, rows behind: more tiles than workgroups that fit the chip, so that
+    # each takes several in a row (inputs of whole 512 entries run on from tile to tile, others start anew)
+    (300, 512, 512, 40, 0, 0),
+    (300, 512, 544, 40, 2, 3),
+    (40, 1024, 1536, 150, 0, 1),
+    (600, 544, 96, 3, 0, 0),
+    (24, 512, 2048, 700, 1, 0),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,latent,inter,per,lead,behind", MANY)
+def test_grouped_many_tiles(k3g, E, latent, inter, per, lead, behind, fmt):
+    """Every product of a large grouped call on the GPU in float64 (the device's own library) from the tests' values."""
+    rng = np.random.default_rng(E + inter)
+    P, k = E * per, 2
+    ex = Experts(k3g, rng, E, latent, inter, 112, 118)
+    off = ragged(rng, E, P, lead, behind, 0.2)
+    perm = rng.permutation(P).astype(np.int32)
+    ac, asc = mx_ref.mx_bytes(rng, (P + 1) // 2, latent, fmt, 118 if fmt == 0 else 112, 126 if fmt == 0 else 118, p255=0.01)
+    hc, hs = mx_ref.mx_bytes(rng, P, inter, fmt, p255=0.01)
+    print(f"many tiles E={E} latent={latent} inter={inter} P={P} fmt={fmt}", flush=True)
+    y = torch.full((P, latent), 7.0, device="cuda")
+    z = torch.full((P, inter), 7.0, device="cuda", dtype=torch.bfloat16)
+    h = k3g.mx_empty(P, inter, k3g.MXFP8)
+    h.codes.fill_(77), h.scales.fill_(9)
+    a = k3g.mx(dev(ac), dev(asc), fmt)
+    k3g.k3g_mx_grouped_matmul(y, k3g.mx(dev(hc), dev(hs), fmt), ex.struct, k3g.W2, dev(off))
+    k3g.k3g_mx_grouped_matmul(z, a, ex.struct, k3g.W3, dev(off), perm=dev(perm), top_k=k)
+    k3g.k3g_mx_grouped_glu(h, a, ex.struct, dev(off), perm=dev(perm), top_k=k)
+    torch.cuda.synchronize()
+    av, hv = dev(mx_ref.values(ac, asc, fmt)), dev(mx_ref.values(hc, hs, fmt))
+    src = dev((perm // k).astype(np.int64))
+    yc, zc, gc, gs = host(y).astype(np.float64), host(z).astype(np.float64), host(h.codes), host(h.scales)
+
+    def product(x, w):
+        w = dev(w).t().contiguous()
+        return (x @ w).cpu().numpy(), (x.abs() @ w.abs()).cpu().numpy()
+    for e in range(E):
+        p0, p1 = int(off[e]), int(off[e + 1])
+        if p1 > p0:
+            check_product(yc[p0:p1], *product(hv[p0:p1], ex.w[2][e]), "f32", f"w2 of expert {e}")
+            x = av[src[p0:p1]]
+            g, ng = product(x, ex.w[0][e])
+            u, nu = product(x, ex.w[1][e])
+            check_product(zc[p0:p1], u, nu, "bf16", f"w3 of expert {e}")
+            if e % 5 == 0:
+                mx_ref.check_quantised(gc[p0:p1], gs[p0:p1], situ64(g, u), situ_tolerance(g, u, ng, nu), 1, f"h of expert {e}")
+    left = np.r_[np.arange(off[0]), np.arange(off[-1], P)]
+    assert np.all(yc[left] == 7.0) and np.all(zc[left] == 7.0) and np.all(gc[left] == 77) and np.all(gs[left] == 9)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,rows,n", [(2100, 4104, 1024), (1025, 8200, 544), (4096, 2304, 512), (700, 12800, 96)])
+def test_matmul_many_tiles(k3g, T, rows, n, fmt):
+    rng = np.random.default_rng(T)
+    ac, asc = mx_ref.mx_bytes(rng, T, n, fmt, p255=0.01)
+    wc, wsc = mx_ref.mx_bytes(rng, rows, n, 0, p255=0.01)
+    print(f"many tiles T={T} rows={rows} in={n} fmt={fmt}", flush=True)
+    y = torch.empty(T, rows, device="cuda")
+    k3g.k3g_mx_matmul(y, k3g.mx(dev(ac), dev(asc), fmt), k3g.mxfp4(dev(wc), dev(wsc)))
+    av, wv = dev(mx_ref.values(ac, asc, fmt)), dev(mx_ref.values(wc, wsc, 0)).t().contiguous()
+    check_product(host(y).astype(np.float64), (av @ wv).cpu().numpy(), (av.abs() @ wv.abs()).cpu().numpy(), "f32", "many tiles")
+
+
 # ---- together, on a side stream, and captured ----------------------------------------------------
 
 def test_experts_from_route_to_combine(k3g):
