@@ -151,25 +151,102 @@ __device__ inline void store_h(const MmArgs &a, int64_t token, int group, const 
     if (q == 0) a.h_scales[at] = fine ? (uint8_t)(e + 127) : (uint8_t)255;
 }
 
-// The expert whose group holds row p, its first row and its end, clipped to
-// the rows of y; false where there is none. Two reads: 64 lanes cut the table
-// into 64 parts, then the part into its entries.
-__device__ inline bool find_group(const MmArgs &a, int p, int &e, int &p0, int &p1) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int step = a.E / kWave + 1;  // 64 * step > E
-    const int i = min(lane * step, a.E);
-    const uint64_t m0 = __ballot(a.offsets[i] <= p);
-    if (!m0) return false;
-    const int base = min((63 - __builtin_clzll(m0)) * step, a.E);
-    const int j = min(base + min(lane, step - 1), a.E);
-    const uint64_t m1 = __ballot(a.offsets[j] <= p);
-    if (!m1) return false;
-    e = __builtin_amdgcn_readfirstlane(min(base + min(63 - __builtin_clzll(m1), step - 1), a.E));
-    if (e >= a.E) return false;
-    p0 = max(__builtin_amdgcn_readfirstlane(a.offsets[e]), 0);
-    p1 = min(__builtin_amdgcn_readfirstlane(a.offsets[e + 1]), a.T);
-    return p0 <= p && p < p1;
-}
+// The work of a launch, item by item: BN rows of y (of one expert) by OUT
+// outputs. Workgroup b runs on XCD b % 8; each XCD takes a contiguous eighth of
+// the items: an expert after another, and in it blocks of outputs by groups of
+// four row tiles, so the workgroups of an XCD that run together read 4 row tiles
+// and a quarter as many blocks of weights as there are of them.
+//
+// Grouped: the constructor (all threads of the workgroup) counts the experts'
+// row tiles into `table` (LDS, E + 1 numbers of tiles before each expert, and 16
+// more for the scan). Groups are clipped to the rows of y; what a table that does
+// not ascend gives more than y has rows for is left out.
+struct Item {
+    int e, p, n_tok, m0;  // expert, first row of y, rows, first output
+};
+template <int MODE, int BN, int OUT>
+struct Items {
+    const MmArgs &a;
+    const int32_t *table;
+    int n_rb, n_tiles, step, near = 0;  // near: an expert at or before the next item's
+    int64_t item, last;
+
+    __device__ inline Items(const MmArgs &a_, int32_t *t, int threads) : a(a_), table(t) {
+        n_rb = (a.rows + OUT - 1) / OUT;
+        if constexpr (MODE == DENSE) {
+            n_tiles = (a.T + BN - 1) / BN;
+        } else {
+            const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+            int32_t *part = t + a.E + 1;
+            const int per = (a.E + threads - 1) / threads, e0 = threadIdx.x * per, e1 = min(e0 + per, a.E);
+            auto tiles = [&](int e) {
+                const int p0 = max(a.offsets[e], 0), p1 = min(a.offsets[e + 1], a.T);
+                return p1 > p0 ? (p1 - p0 + BN - 1) / BN : 0;
+            };
+            int n = 0;
+            for (int e = e0; e < e1; ++e) n += tiles(e);
+            int x = n;
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == kWave - 1) part[wave] = x;
+            __syncthreads();
+            int before = x - n;
+            for (int w = 0; w < wave; ++w) before += part[w];
+            for (int e = e0; e < e1; ++e) {
+                t[e] = before;
+                before += tiles(e);
+            }
+            if (e0 < a.E && e1 == a.E) t[a.E] = before;
+            __syncthreads();
+            n_tiles = min(__builtin_amdgcn_readfirstlane(t[a.E]), a.T / BN + min(a.E, a.T));
+        }
+        const int64_t n_items = (int64_t)n_tiles * n_rb;
+        const int xcd = blockIdx.x % 8;
+        step = gridDim.x / 8;
+        last = n_items * (xcd + 1) / 8;
+        item = n_items * xcd / 8 + blockIdx.x / 8;
+    }
+
+    // The next item that has rows (in an ascending table all have); whole wavefronts call it.
+    __device__ inline bool next(Item &o) {
+        for (; item < last; item += step) {
+            int t0 = 0, nt = n_tiles;
+            o.e = 0;
+            if constexpr (MODE != DENSE) {
+                const int tile = (int)(item / n_rb), lane = threadIdx.x & (kWave - 1);
+                // experts after `near` whose first tile is at most this one, 64 at a time
+                for (;;) {
+                    const int i = near + 1 + lane;
+                    const int n = __popcll(__ballot(i < a.E && table[min(i, a.E)] <= tile));
+                    near += n;
+                    if (n < kWave) break;
+                }
+                near = __builtin_amdgcn_readfirstlane(near);
+                o.e = near;
+                t0 = __builtin_amdgcn_readfirstlane(table[near]);
+                nt = __builtin_amdgcn_readfirstlane(table[near + 1]) - t0;
+            }
+            const int64_t in_expert = item - (int64_t)t0 * n_rb;
+            const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
+            if (wide < 1) continue;
+            const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
+            o.m0 = in_group / wide * OUT;
+            o.p = (group * 4 + in_group % wide) * BN;
+            int end = a.T;
+            if constexpr (MODE != DENSE) {
+                o.p += max(__builtin_amdgcn_readfirstlane(a.offsets[o.e]), 0);
+                end = min(__builtin_amdgcn_readfirstlane(a.offsets[o.e + 1]), a.T);
+            }
+            o.n_tok = min(BN, end - o.p);
+            if (o.p < 0 || o.n_tok < 1 || o.m0 >= a.rows) continue;
+            item += step;
+            return true;
+        }
+        return false;
+    }
+};
 
 // The activations' row behind row p of y.
 __device__ inline int source_row(const MmArgs &a, int p) {

@@ -15,116 +15,216 @@
 // and its scale made finite: it adds exactly nothing.
 #include "mxmm.h"
 
+#ifndef K3G_STREAM_WGS
+#define K3G_STREAM_WGS 4
+#endif
+#ifndef K3G_NT1
+#define K3G_NT1 16
+#endif
+#ifndef K3G_NT2
+#define K3G_NT2 32
+#endif
+#ifndef K3G_NT4
+#define K3G_NT4 256
+#endif
+
 namespace k3g {
 
 // ---- few tokens: the weights streamed once -----------------------------------------
 //
-// A workgroup takes 16 tokens (of one expert) and 32 outputs (GLU: 32 rows of
-// w1 and the same 32 of w3), its eight wavefronts every eighth step of 128
-// entries each; the partial sums meet in LDS, added in wavefront order.
-constexpr int kStreamWaves = 8;
+// A workgroup takes up to 16 NT tokens (of one expert) and 32 outputs (GLU: 32
+// rows of w1 and the same 32 of w3), each wavefront four steps of 128 entries at
+// a time: their weights and scales are all in flight before the first product
+// (16 KB a wavefront in the GLU). The wavefronts' sums meet in LDS and are added
+// in wavefront order. Four consecutive lanes load 64 contiguous bytes of a row
+// (the L2 serves that several times faster than 16 rows in consecutive lanes) and
+// a permutation brings them into operand order.
+constexpr int kSteps = 4;       // steps a wavefront loads together
+constexpr int kStreamWaves = 8;  // most wavefronts of a workgroup
 
-template <int AF, int MODE>
+template <int AF, int MODE_, int NT_>
+struct Stream {
+    static constexpr int MODE = MODE_, NT = NT_, TILES = MODE == GLU ? 4 : 2, BN = 16 * NT, OUT = 32;
+    static constexpr int part(int waves) { return waves * TILES * NT * kWave * 16; }
+    static constexpr int lds(int waves, int E) { return part(waves) + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
+};
+
+// Sixteen scale bytes of a row from group g on (255 past the row's end).
+__device__ inline uint4 scales16(const uint8_t *row, int g, int G) {
+    uint4 v = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (g + 16 <= G) {
+        __builtin_memcpy(&v, row + g, 16);
+    } else {
+        uint8_t b[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) b[k] = g + k < G ? row[min(g + k, G - 1)] : 255;
+        __builtin_memcpy(&v, b, 16);
+    }
+    return v;
+}
+__device__ inline uint32_t dword(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <int AF, class C>
 __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs a) {
-    constexpr int TILES = MODE == GLU ? 4 : 2;
-    __shared__ float4_t part[kStreamWaves][TILES][kWave];
+    constexpr int TILES = C::TILES, NT = C::NT, AH = AF == K3G_MXFP4 ? 1 : 2;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int waves = blockDim.x / kWave;
+    float4_t *part = (float4_t *)lds;  // [wave][tile][token tile][lane]
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r = lane & 15, q = lane >> 4;
-    const int row0 = blockIdx.x * 32;
-    const int64_t w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
-    for (int64_t tile = blockIdx.y;; tile += gridDim.y) {
-        int e = 0, p, end;
-        if constexpr (MODE == DENSE) {
-            if (tile * 16 >= a.T) return;
-            p = (int)(tile * 16);
-            end = a.T;
-        } else {
-            if (tile >= a.T) return;
-            int p0;
-            p = (int)tile;
-            if (!find_group(a, p, e, p0, end) || (p - p0) % 16) continue;
-        }
-        const int n_tok = min(16, end - p);
-        const int64_t src = MODE == DENSE ? p + min(r, n_tok - 1) : source_row(a, p + min(r, n_tok - 1));
-        const uint8_t *ac = a.a_codes + src * a_pitch, *as = a.a_scales + src * a.G;
-        const uint8_t *wc[TILES], *wsc[TILES];
+    const int r = lane & 15, q = lane >> 4;     // as the operand has them
+    const int lr = lane >> 2, lq = lane & 3;    // as they are loaded
+    const int psrc = 4 * (4 * r + q);
+    const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
+    const int S = (a.G + 3) / 4;
+    Items<C::MODE, C::BN, C::OUT> items(a, (int32_t *)(lds + C::part(waves)), blockDim.x);
+    Item it;
+    while (items.next(it)) {
+        const uint8_t *wc[TILES], *wsc[TILES], *ac[NT], *asc[NT];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int64_t row = min(row0 + pair_row(r, t & 1), a.rows - 1);
-            wc[t] = a.w[t >> 1] + e * a.stride + row * w_pitch;
-            wsc[t] = a.ws[t >> 1] + e * a.stride + row * a.G;
+            const int64_t first = it.e * a.stride;
+            wc[t] = a.w[t >> 1] + first + (int64_t)min(it.m0 + pair_row(lr, t & 1), a.rows - 1) * w_pitch;
+            wsc[t] = a.ws[t >> 1] + first + (int64_t)min(it.m0 + pair_row(r, t & 1), a.rows - 1) * a.G;
         }
-        float4_t acc[TILES];
+        float4_t acc[TILES][NT];
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-        for (int g0 = 4 * wave; g0 < a.G; g0 += 4 * kStreamWaves) {
-            const int g = g0 + q;
-            const int gc = min(g, a.G - 1);
-            uint32_t sa = g < a.G ? as[gc] : 255u;
-            const Act<AF> B = [&] {
-                if constexpr (AF == K3G_MXFP4) {
-                    return Act<AF>(keep4(load16(ac + 16 * gc), sa != 255u));
-                } else {
-                    // this lane's bytes belong to the groups q/2 and 2 + q/2
-                    const int g1 = g0 + (q >> 1), g2 = g1 + 2, g1c = min(g1, a.G - 1), g2c = min(g2, a.G - 1);
-                    return Act<AF>(keep4(load16(ac + 32 * g1c + 16 * (q & 1)), g1 < a.G && as[g1c] != 255u),
-                                   keep4(load16(ac + 32 * g2c + 16 * (q & 1)), g2 < a.G && as[g2c] != 255u));
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+        const int nf = (it.n_tok + 15) / 16;  // token tiles with tokens
+        bool first = true;
+        for (int s0 = kSteps * wave; s0 < S; s0 += kSteps * waves) {
+            uint4 w[kSteps][TILES], sw[TILES];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) sw[t] = scales16(wsc[t], 4 * s0, a.G);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+                    w[i][t] = load16(wc[t] + 16 * (int64_t)min(4 * (s0 + i) + lq, a.G - 1));
+            if (first) {  // (behind the first loads of the weights)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int64_t load = source_row(a, it.p + min(16 * j + lr, it.n_tok - 1));
+                    const int64_t row = source_row(a, it.p + min(16 * j + r, it.n_tok - 1));
+                    ac[j] = a.a_codes + load * a_pitch;
+                    asc[j] = a.a_scales + row * a.G;
                 }
-            }();
-            sa = sa == 255u ? 127u : sa;
-            __asm__ volatile("" : "+v"(sa));
+                first = false;
+            }
+            uint4 sa[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sa[j] = scales16(asc[j], 4 * s0, a.G);
+            uint4 b[2][NT][AH];
+            auto load_b = [&](int i) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int h = 0; h < AH; ++h) {
+                        // e4m3: half h of a step's 128 bytes, in chunks of half a group
+                        const int c = AH * 4 * (s0 + i) + 4 * h + lq;
+                        b[i & 1][j][h] = load16(ac[j] + 16 * (int64_t)min(c, AH * a.G - 1));
+                    }
+            };
+            load_b(0);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                if (s0 + i >= S) break;
+                if (i + 1 < kSteps) load_b(i + 1);
+                v8i_t W[TILES];
+                uint32_t ws[TILES];
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    uint32_t s = (dword(sw[t], i) >> (8 * q)) & 255u;
+                    const uint4 v = keep4(to_operand(w[i][t], psrc), s != 255u);
+                    W[t] = v8i_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+                    ws[t] = s == 255u ? 127u : s;
+                    __asm__ volatile("" : "+v"(ws[t]));
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    if (NT > 1 && j >= nf) break;
+                    const uint32_t d = dword(sa[j], i);
+                    uint32_t s = (d >> (8 * q)) & 255u;
+                    const Act<AF> B = [&] {
+                        if constexpr (AF == K3G_MXFP4)
+                            return Act<AF>(keep4(to_operand(b[i & 1][j][0], psrc), s != 255u));
+                        else  // this lane's bytes belong to the groups q/2 and 2 + q/2
+                            return Act<AF>(
+                                keep4(to_operand(b[i & 1][j][0], psrc), ((d >> (8 * (q >> 1))) & 255u) != 255u),
+                                keep4(to_operand(b[i & 1][j][1], psrc), ((d >> (16 + 8 * (q >> 1))) & 255u) != 255u));
+                    }();
+                    s = s == 255u ? 127u : s;
+                    __asm__ volatile("" : "+v"(s));
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) acc[t][j] = B.mul(W[t], acc[t][j], ws[t], s);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) part[((wave * TILES + t) * NT + j) * kWave + lane] = acc[t][j];
+        __syncthreads();
+        for (int j = wave; j < nf; j += waves) {  // a wavefront sums a token tile
+            float4_t s[TILES];
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
-                uint32_t sw = g < a.G ? wsc[t][gc] : 255u;
-                const uint4 w = keep4(load16(wc[t] + 16 * gc), sw != 255u);
-                sw = sw == 255u ? 127u : sw;
-                __asm__ volatile("" : "+v"(sw));
-                acc[t] = B.mul(v8i_t{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0}, acc[t], sw, sa);
+                s[t] = part[(t * NT + j) * kWave + lane];
+                for (int v = 1; v < waves; ++v) s[t] += part[((v * TILES + t) * NT + j) * kWave + lane];
             }
-        }
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) part[wave][t][lane] = acc[t];
-        __syncthreads();
-        auto sum = [&](int t) {
-            float4_t s = part[0][t][lane];
-#pragma unroll
-            for (int w = 1; w < kStreamWaves; ++w) s += part[w][t][lane];
-            return s;
-        };
-        if constexpr (MODE == GLU) {
-            if (wave == 0) {
+            const bool live = 16 * j + r < it.n_tok;
+            const int64_t token = it.p + 16 * j + r;
+            if constexpr (C::MODE == GLU) {
                 float4_t h[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float4_t g = sum(t), u = sum(2 + t);
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[t][i] = situ(g[i], u[i]);
-                }
-                const bool live = r < n_tok;  // a.rows is a multiple of 32
+                    for (int i = 0; i < 4; ++i) h[t][i] = situ(s[t][i], s[2 + t][i]);
+                // (a.rows is a multiple of 32)
                 if (a.h_format == K3G_MXFP4)
-                    store_h<K3G_MXFP4>(a, p + r, row0 / kGroup, h[0], h[1], live);
+                    store_h<K3G_MXFP4>(a, token, it.m0 / kGroup, h[0], h[1], live);
                 else
-                    store_h<K3G_MXFP8>(a, p + r, row0 / kGroup, h[0], h[1], live);
+                    store_h<K3G_MXFP8>(a, token, it.m0 / kGroup, h[0], h[1], live);
+            } else {
+                const int row = it.m0 + 8 * q;
+                if (live) with_store(a, [&](auto store) { store(token * a.ys + row, a.rows - row, s[0], s[1]); });
             }
-        } else if (wave == 0) {
-            const float4_t lo = sum(0), hi = sum(1);
-            const int row = row0 + 8 * q;
-            if (r < n_tok) with_store(a, [&](auto store) { store((p + r) * a.ys + row, a.rows - row, lo, hi); });
         }
-        __syncthreads();  // part is read before the next tile writes it
+        __syncthreads();  // part is read before the next item writes it
     }
 }
 
-template <int MODE>
-int launch_stream(const MmArgs &a, int af, hipStream_t st) {
-    if (MODE == DENSE ? a.T > 32 : a.T > 4 * a.E) return launch_tile(a, MODE, af, st);
-    const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 15) / 16 : a.T;
-    const dim3 grid((a.rows + 31) / 32, (unsigned)(tiles < 65535 ? tiles : 65535));
-    if (af == K3G_MXFP4)
-        mx_stream_kernel<K3G_MXFP4, MODE><<<grid, kStreamWaves * kWave, 0, st>>>(a);
-    else
-        mx_stream_kernel<K3G_MXFP8, MODE><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+template <int AF, class C>
+int launch_stream(const MmArgs &a, hipStream_t st) {
+    const int chunks = ((a.G + 3) / 4 + kSteps - 1) / kSteps;
+    const int waves = chunks < kStreamWaves ? chunks : kStreamWaves;
+    const int bytes = C::lds(waves, a.E);
+    if (bytes > 65536 && hipFuncSetAttribute((const void *)mx_stream_kernel<AF, C>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return K3G_EHIP;
+    const int64_t n_rb = (a.rows + C::OUT - 1) / C::OUT;
+    const int64_t tiles = C::MODE == DENSE ? ((int64_t)a.T + C::BN - 1) / C::BN
+                                           : a.T / C::BN + (a.E < a.T ? a.E : a.T);
+    const int64_t items = tiles * n_rb, most = 256 * K3G_STREAM_WGS, grid = items < most ? (items + 7) / 8 * 8 : most;
+    mx_stream_kernel<AF, C><<<(unsigned)grid, waves * kWave, bytes, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+}
+
+// Which kernel: rules on the rows (of the whole call, or an expert on average).
+template <int AF, int MODE>
+int launch_product(const MmArgs &a, hipStream_t st) {
+    if constexpr (MODE == DENSE) {
+        if (a.T <= K3G_NT1) return launch_stream<AF, Stream<AF, MODE, 1>>(a, st);
+        if (a.T <= K3G_NT2) return launch_stream<AF, Stream<AF, MODE, 2>>(a, st);
+        if (a.T <= K3G_NT4) return launch_stream<AF, Stream<AF, MODE, 4>>(a, st);
+    }
+    return launch_tile(a, MODE, AF, st);
+}
+
+template <int MODE>
+int launch_any(const MmArgs &a, int af, hipStream_t st) {
+    return af == K3G_MXFP4 ? launch_product<K3G_MXFP4, MODE>(a, st) : launch_product<K3G_MXFP8, MODE>(a, st);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -207,7 +307,7 @@ int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const 
     m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, w->rows);
     m.T = a->rows, m.rows = w->rows, m.in = a->in, m.G = a->in / kGroup;
     m.odd = odd_scales(m);
-    return launch_stream<DENSE>(m, a->format, (hipStream_t)stream);
+    return launch_any<DENSE>(m, a->format, (hipStream_t)stream);
 }
 
 int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_expert_bank *bank,
@@ -235,7 +335,7 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
     m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, d.rows);
     m.T = n_rows, m.rows = d.rows, m.in = d.in, m.G = d.in / kGroup;
     m.odd = odd_scales(m);
-    return launch_stream<GROUPED>(m, a->format, (hipStream_t)stream);
+    return launch_any<GROUPED>(m, a->format, (hipStream_t)stream);
 }
 
 int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *bank, const int32_t *offsets,
@@ -267,7 +367,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
     m.h_codes = h->codes, m.h_scales = h->scales, m.h_format = h->format;
     m.T = n_rows, m.rows = bank->inter, m.in = bank->latent, m.G = bank->latent / kGroup;
     m.odd = odd_scales(m);
-    return launch_stream<GLU>(m, a->format, (hipStream_t)stream);
+    return launch_any<GLU>(m, a->format, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -36,10 +36,12 @@ struct Tile {
     static constexpr int BM = WR * FM * 16, BN = WC * FN * 16;
     static constexpr int OUT = MODE == GLU ? BM / 2 : BM;  // outputs of a tile
     static constexpr int AB = AF == K3G_MXFP4 ? 64 : 128;  // bytes of a token a stage
-    static constexpr int MW = BM / NW, MA = BN / NW;       // rows that a wavefront loads and prepares
+    // Rows that a wavefront loads and prepares; with fewer than 16 tokens for each, several load the
+    // same ones to the same place.
+    static constexpr int MW = BM / NW, MA = BN / NW < 16 ? 16 : BN / NW;
     static constexpr int DW = MW / 16, DA = MA * AB / 1024;  // DMA instructions of 1 KB
     static_assert(MW % 16 == 0 && MA % 16 == 0 && MW + MA <= kWave, "a lane for each row of a wavefront");
-    static_assert(FM % 4 == 0 && FN % 2 == 0, "halves; GLU: a wavefront owns whole 32-groups of h");
+    static_assert(FM % 4 == 0 && (FN == 1 || FN % 2 == 0), "halves; GLU: a wavefront owns whole 32-groups of h");
     static constexpr int V = DW + DA, X = ODD ? 5 : 1;  // loads of a stage, and of four stages' scales
     static_assert(NB >= 2 && NB <= 4, "the scales of four stages are prepared before the next four's are loaded");
     // LDS: data per stage, raw scales of four stages, scales in operand order
@@ -49,8 +51,8 @@ struct Tile {
     static constexpr int PERM_AT = SCALES_AT + SCALES;  // grouped: the next tile's source rows, and the table
     static constexpr int TABLE = PERM_AT + (MODE == DENSE ? 0 : NW * kWave * 4);
     static constexpr int lds(int E) { return TABLE + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
-    static constexpr int WGS = lds(900) <= 81920 ? 2 : 1;
-    static constexpr int WAVES = THREADS / 256 * WGS < 2 ? 1 : 2;  // wavefronts per SIMD that the registers allow for
+    static constexpr int WGS = 163840 / lds(900);  // workgroups on a CU
+    static constexpr int WAVES = NW * WGS < 8 ? 1 : 2;  // wavefronts per SIMD that the registers allow for
     // loads in flight behind stage s+1 (s % 4 = ph): stages s+2 .. s+NB-1
     static constexpr int behind(int ph) {
         int n = (NB - 2) * V;
@@ -133,97 +135,15 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wr = wave / C::WC, wc = wave % C::WC;
     const uint32_t lds0 = lds_addr(lds);
-    const int n_rb = (a.rows + C::OUT - 1) / C::OUT;
-    int32_t *table = (int32_t *)(lds + C::TABLE);  // grouped: first tile of each expert, [E] the number of tiles
-
-    int n_tiles;
-    if constexpr (C::MODE == DENSE) {
-        n_tiles = (a.T + C::BN - 1) / C::BN;
-    } else {
-        // tiles before each expert: every thread counts those of `per` experts,
-        // then a scan over the wavefront's lanes and over the wavefronts
-        int32_t *part = table + a.E + 1;
-        const int per = (a.E + C::THREADS - 1) / C::THREADS, e0 = threadIdx.x * per;
-        int n = 0;
-        for (int e = e0; e < min(e0 + per, a.E); ++e) {
-            const int p0 = max(a.offsets[e], 0), p1 = min(a.offsets[e + 1], a.T);
-            n += p1 > p0 ? (p1 - p0 + C::BN - 1) / C::BN : 0;
-        }
-        int x = n;
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int y = __shfl_up(x, d);
-            if (lane >= d) x += y;
-        }
-        if (lane == kWave - 1) part[wave] = x;
-        __syncthreads();
-        int before = x - n;
-        for (int w = 0; w < wave; ++w) before += part[w];
-        for (int e = e0; e < min(e0 + per, a.E); ++e) {
-            table[e] = before;
-            const int p0 = max(a.offsets[e], 0), p1 = min(a.offsets[e + 1], a.T);
-            before += p1 > p0 ? (p1 - p0 + C::BN - 1) / C::BN : 0;
-        }
-        if (e0 < a.E && e0 + per >= a.E) table[a.E] = before;
-        __syncthreads();
-        // (ascending groups have no more tiles than this)
-        n_tiles = min(__builtin_amdgcn_readfirstlane(table[a.E]), a.T / C::BN + min(a.E, a.T));
-    }
-
-    // Workgroup b runs on XCD b % 8; each XCD takes a contiguous eighth of the
-    // items: an expert after another, and in it row blocks by groups of four
-    // token tiles, so the workgroups of an XCD that run together read 4 token
-    // tiles and a quarter as many row blocks as there are of them.
-    const int64_t n_items = (int64_t)n_tiles * n_rb;
-    const int xcd = blockIdx.x % 8, step = gridDim.x / 8;
-    const int64_t last = n_items * (xcd + 1) / 8;
-    struct Item {
-        int e, p, n_tok, m0;
-    };
-    int near = 0;  // an expert at or before the next item's
-    // the first item from `item` on that has tokens (all have, in an ascending table); its successor in `item`
-    auto next_item = [&](int64_t &item, Item &o) {
-        for (; item < last; item += step) {
-            int t0 = 0, nt = n_tiles;
-            o.e = 0;
-            if constexpr (C::MODE != DENSE) {
-                const int tile = (int)(item / n_rb);
-                // experts after `near` whose first tile is at most this one, 64 at a time
-                for (;;) {
-                    const int i = near + 1 + lane;
-                    const int n = __popcll(__ballot(i < a.E && table[min(i, a.E)] <= tile));
-                    near += n;
-                    if (n < kWave) break;
-                }
-                near = __builtin_amdgcn_readfirstlane(near);
-                o.e = near;
-                t0 = __builtin_amdgcn_readfirstlane(table[near]);
-                nt = __builtin_amdgcn_readfirstlane(table[near + 1]) - t0;
-            }
-            const int64_t in_expert = item - (int64_t)t0 * n_rb;
-            const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
-            if (wide < 1) continue;
-            const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
-            o.m0 = in_group / wide * C::OUT;
-            o.p = (group * 4 + in_group % wide) * C::BN;
-            int end = a.T;
-            if constexpr (C::MODE != DENSE) {
-                o.p += max(__builtin_amdgcn_readfirstlane(a.offsets[o.e]), 0);
-                end = min(__builtin_amdgcn_readfirstlane(a.offsets[o.e + 1]), a.T);
-            }
-            o.n_tok = min(C::BN, end - o.p);
-            if (o.p < 0 || o.n_tok < 1 || o.m0 >= a.rows) continue;
-            item += step;
-            return true;
-        }
-        return false;
-    };
+    Items<C::MODE, C::BN, C::OUT> items(a, (int32_t *)(lds + C::TABLE), C::THREADS);
+    Item now, next;
 
     // ---- what this wavefront loads: MW weight rows from row MW * wave, MA tokens from MA * wave
     const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
     const int S = (a.G + 3) / 4, Gt = a.G - 4 * (S - 1);  // stages, groups of the last
     const bool is_w = lane < C::MW, has_row = lane < C::MW + C::MA;
     const int iw = wave * C::MW + min(lane, C::MW - 1), ia_own = min(max(lane - C::MW, 0), C::MA - 1);
-    const int ia = wave * C::MA + ia_own;
+    const int a0 = wave * C::MA % C::BN, ia = a0 + ia_own;
     const int cw = (lane & 3) ^ w_swz(lane >> 2);                     // the chunk this lane moves, of row lane / 4
     const int ca = AF == K3G_MXFP4 ? (lane & 3) ^ ((lane >> 3) & 3)  // ... of a token
                                    : (lane & 7) ^ (lane >> 3);
@@ -236,7 +156,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     int32_t *perm = (int32_t *)(lds + C::PERM_AT) + wave * kWave;
     auto fetch_perm = [&](const Item &o) {
         if (C::MODE != DENSE && a.perm && lane < C::MA)
-            dma4_at(a.perm + o.p + min(wave * C::MA + lane, o.n_tok - 1), lds0 + C::PERM_AT + wave * kWave * 4);
+            dma4_at(a.perm + o.p + min(a0 + lane, o.n_tok - 1), lds0 + C::PERM_AT + wave * kWave * 4);
     };
     auto address = [&](const Item &o) {
         auto w_row = [&](int i) {  // row past m0 of row i of the tile
@@ -245,7 +165,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
         };
         const bool gather = C::MODE != DENSE && a.perm;
         auto a_row = [&](int own) {  // row past ba of this wavefront's token `own`
-            if (!gather) return min(wave * C::MA + own, o.n_tok - 1);
+            if (!gather) return min(a0 + own, o.n_tok - 1);
             return min(max(perm[own] / a.top_k, 0), a.a_rows - 1);
         };
         ba = gather ? a.a_codes : a.a_codes + (int64_t)o.p * a_pitch;
@@ -272,7 +192,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             dma16(bw[d] + 64 * (int64_t)s, vw[d] - backw, buf + (wave * C::MW + 16 * d) * 64);
 #pragma unroll
         for (int d = 0; d < C::DA; ++d)
-            dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + wave * C::MA * C::AB + 1024 * d);
+            dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + a0 * C::AB + 1024 * d);
     };
     const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
     auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
@@ -348,7 +268,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     // Operands of a stage in two halves: by weight rows, the tokens' tiles whole and
     // in two sets (now, next), or by tokens with the weights' whole: an e4m3
     // tile is cut in two for the matrix cores, which is done once that way.
-    constexpr bool BY_ROWS = AF == K3G_MXFP4;
+    constexpr bool BY_ROWS = AF == K3G_MXFP4 || C::FN == 1;
     constexpr int HM = BY_ROWS ? C::FM / 2 : C::FM, HN = BY_ROWS ? C::FN : C::FN / 2;
     uint4 wt[2][HM], tk[2][HN][C::AB / 64];
     uint32_t sw[C::FM], st[C::FN];
@@ -396,12 +316,10 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     // Rows of whole four stages run on from item to item: the last NB stages of
     // one issue the first of the next, which land behind its way out.
     const bool run_on = S % 4 == 0 && S >= C::NB;
-    int64_t item = n_items * xcd / 8 + blockIdx.x / 8;
-    Item now, next;
-    bool have = next_item(item, now), loaded = false;  // loaded: its first NB stages are in LDS, stage 0 prepared
+    bool have = items.next(now), loaded = false;  // loaded: its first NB stages are in LDS, stage 0 prepared
     int at = 0;                                          // the buffer of the stage being multiplied
     while (have) {
-        const bool more = next_item(item, next), on = run_on && more;
+        const bool more = items.next(next), on = run_on && more;
         if (!loaded) {
             fetch_perm(now);
             wait_vm<0>();
@@ -560,8 +478,17 @@ int launch(const MmArgs &a, hipStream_t st) {
 #ifndef K3G_LOW_PER
 #define K3G_LOW_PER 32
 #endif
+#ifndef K3G_TILE_TINY
+#define K3G_TILE_TINY 2, 2, 4, 1, 4
+#endif
+#ifndef K3G_TINY_PER
+#define K3G_TINY_PER 8
+#endif
 template <int AF, int MODE, bool ODD>
 int launch_mode(const MmArgs &a, hipStream_t st) {
+    if constexpr (MODE != DENSE) {
+        if (a.T <= K3G_TINY_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_TINY, ODD>>(a, st);
+    }
     if (MODE == DENSE ? a.T <= 64 : a.T <= K3G_LOW_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
     if constexpr (AF == K3G_MXFP4 && MODE == DENSE) {
         if ( (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
