@@ -445,7 +445,7 @@ class Mx:
     """A microscaled matrix (k3g_mx): codes uint8 [rows, in/2] (MXFP4) or
     [rows, in] (MXFP8), scales uint8 [rows, in/32], and their format."""
 
-    __slots__ = ("codes", "scales", "format", "rows", "n_in", "struct")
+    __slots__ = ("codes", "scales", "format", "rows", "n_in", "device", "struct", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int):
         if fmt not in (MXFP4, MXFP8):
@@ -454,13 +454,18 @@ class Mx:
         _dev(scales, torch.uint8, "scales")
         if codes.dim() != 2:
             raise ValueError("codes must be [rows, in/2] (MXFP4) or [rows, in] (MXFP8)")
-        self.rows, self.n_in = codes.shape[0], codes.shape[1] * (2 if fmt == MXFP4 else 1)
-        if self.n_in % GROUP or tuple(scales.shape) != (self.rows, self.n_in // GROUP):
+        n_in = codes.shape[1] * (2 if fmt == MXFP4 else 1)
+        if n_in % GROUP or tuple(scales.shape) != (codes.shape[0], n_in // GROUP):
             raise ValueError("scales must be [rows, in/32]")
         if scales.device != codes.device:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales, self.format = codes, scales, fmt
-        self.struct = MxStruct(codes.data_ptr(), scales.data_ptr(), self.rows, self.n_in, fmt)
+        self._set(codes, scales, fmt, codes.shape[0], n_in)
+
+    def _set(self, codes, scales, fmt, rows, n_in):
+        self.codes, self.scales, self.format, self.rows, self.n_in = codes, scales, fmt, rows, n_in
+        self.device = codes.get_device()
+        self.struct = MxStruct(codes.data_ptr(), scales.data_ptr(), rows, n_in, fmt)
+        self._ref = C.byref(self.struct)
 
 
 def mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int) -> Mx:
@@ -469,38 +474,53 @@ def mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int) -> Mx:
 
 
 def mx_empty(rows: int, n_in: int, fmt: int, device="cuda") -> Mx:
-    """A microscaled matrix of that size, not initialised."""
+    """A microscaled matrix of that size, not initialised (codes, then scales, in one piece of memory)."""
     if fmt not in (MXFP4, MXFP8) or rows < 0 or n_in <= 0 or n_in % GROUP:
         raise ValueError("invalid microscaled shape or format")
-    return Mx(torch.empty((rows, n_in // 2 if fmt == MXFP4 else n_in), dtype=torch.uint8, device=device),
-              torch.empty((rows, n_in // GROUP), dtype=torch.uint8, device=device), fmt)
+    wide, groups = n_in // 2 if fmt == MXFP4 else n_in, n_in // GROUP
+    at = rows * wide  # a multiple of 16
+    buf = torch.empty(at + rows * groups, dtype=torch.uint8, device=device)
+    codes = buf.as_strided((rows, wide), (wide, 1))
+    scales = buf.as_strided((rows, groups), (groups, 1), at)
+    if buf.device.type != "cuda":
+        return Mx(codes, scales, fmt)  # refused there
+    q = Mx.__new__(Mx)
+    q._set(codes, scales, fmt, rows, n_in)
+    return q
 
 
-def _rows(t: torch.Tensor, name: str, shape=None, dtype=None):
+def _rows(t: torch.Tensor, name: str, rows: int = -1, cols: int = -1, dtype=None) -> int:
     """A dense operand [rows, cols]: rows may lie apart, entries may not. Returns its row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if t.get_device() < 0:
         raise ValueError(f"{name} must live on the GPU")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be {list(shape) if shape else '[rows, cols]'}, got {list(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols], got {list(t.shape)}")
+    n, m = t.shape
+    if (rows >= 0 and n != rows) or (cols >= 0 and m != cols):
+        raise ValueError(f"{name} must be {[rows, cols]}, got {[n, m]}")
+    if n <= 1:
+        if m > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have its entries side by side")
+        return m
+    ld, one = t.stride()
+    if one != 1 and m > 1:
         raise ValueError(f"{name} must have its entries side by side")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
+    if ld < m:
         raise ValueError(f"{name}'s rows must not overlap")
-    return t.stride(0)
+    return ld
 
 
-def _here(*tensors):
-    """The launch goes to the current device: every tensor has to be there."""
+def _launch_stream(stream, *devices) -> int:
+    """The stream to launch on. The launch goes to the current device: every tensor has to be there."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+    for d in devices:
+        if d != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got cuda:{d}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _mx_arg(q, name: str) -> Mx:
@@ -512,20 +532,18 @@ def _mx_arg(q, name: str) -> Mx:
 def k3g_mx_quantize(q: Mx, x: torch.Tensor, stream=None) -> Mx:
     """x [rows, in] (float32, bfloat16 or float16; rows may lie apart) -> q, per 32-group."""
     _mx_arg(q, "q")
-    ld = _rows(x, "x", (q.rows, q.n_in))
-    _here(x, q.codes)
-    _check("k3g_mx_quantize", lib().k3g_mx_quantize(C.byref(q.struct), x.data_ptr(), _TYPES[x.dtype], ld,
-                                                     _stream(stream)))
+    ld = _rows(x, "x", q.rows, q.n_in)
+    st = _launch_stream(stream, x.get_device(), q.device)
+    _check("k3g_mx_quantize", lib().k3g_mx_quantize(q._ref, x.data_ptr(), _TYPES[x.dtype], ld, st))
     return q
 
 
 def k3g_mx_dequantize(y: torch.Tensor, q: Mx, stream=None) -> torch.Tensor:
     """q's values, rounded once to y's type."""
     _mx_arg(q, "q")
-    ld = _rows(y, "y", (q.rows, q.n_in))
-    _here(y, q.codes)
-    _check("k3g_mx_dequantize", lib().k3g_mx_dequantize(y.data_ptr(), _TYPES[y.dtype], ld, C.byref(q.struct),
-                                                         _stream(stream)))
+    ld = _rows(y, "y", q.rows, q.n_in)
+    st = _launch_stream(stream, y.get_device(), q.device)
+    _check("k3g_mx_dequantize", lib().k3g_mx_dequantize(y.data_ptr(), _TYPES[y.dtype], ld, q._ref, st))
     return y
 
 
@@ -541,15 +559,23 @@ def k3g_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, r: torch.T
         raise ValueError("gamma must have one entry a column")
     if y is None and q is None:
         raise ValueError("at least one of y and q")
-    one = {}
-    for name, t in (("r", r), ("sum", sum), ("y", y)):
-        one[name] = (t.data_ptr(), _rows(t, name, (n, n_in), x.dtype)) if t is not None else (None, 0)
-    if q is not None and (_mx_arg(q, "q").rows, q.n_in) != (n, n_in):
-        raise ValueError("q must have x's rows and columns")
-    _here(x, gamma, r, sum, y, None if q is None else q.codes)
-    _check("k3g_add_rmsnorm", lib().k3g_add_rmsnorm(*one["y"], *one["sum"], None if q is None else C.byref(q.struct),
-                                                     x.data_ptr(), ld, *one["r"], _TYPES[x.dtype], gamma.data_ptr(),
-                                                     eps, n, n_in, _stream(stream)))
+    devices = [x.get_device(), gamma.get_device()]
+    one = []
+    for name, t in (("y", y), ("sum", sum), ("r", r)):
+        if t is None:
+            one.append((None, 0))
+        else:
+            one.append((t.data_ptr(), _rows(t, name, n, n_in, x.dtype)))
+            devices.append(t.get_device())
+    ref = None
+    if q is not None:
+        if (_mx_arg(q, "q").rows, q.n_in) != (n, n_in):
+            raise ValueError("q must have x's rows and columns")
+        devices.append(q.device)
+        ref = q._ref
+    st = _launch_stream(stream, *devices)
+    _check("k3g_add_rmsnorm", lib().k3g_add_rmsnorm(*one[0], *one[1], ref, x.data_ptr(), ld, *one[2], _TYPES[x.dtype],
+                                                     gamma.data_ptr(), eps, n, n_in, st))
     return sum, y, q
 
 
@@ -558,26 +584,30 @@ def k3g_mx_matmul(y: torch.Tensor, a: Mx, w: Mxfp4, stream=None) -> torch.Tensor
     _mx_arg(a, "a")
     if w.in_ != a.n_in:
         raise ValueError("shape mismatch")
-    ld = _rows(y, "y", (a.rows, w.rows))
-    _here(y, a.codes, *getattr(w, "_keep", ()))
-    _check("k3g_mx_matmul", lib().k3g_mx_matmul(y.data_ptr(), _TYPES[y.dtype], ld, C.byref(a.struct), C.byref(w),
-                                                 _stream(stream)))
+    ld = _rows(y, "y", a.rows, w.rows)
+    st = _launch_stream(stream, y.get_device(), a.device, *[t.get_device() for t in getattr(w, "_keep", ())])
+    _check("k3g_mx_matmul", lib().k3g_mx_matmul(y.data_ptr(), _TYPES[y.dtype], ld, a._ref, C.byref(w), st))
     return y
 
 
-def _groups(a: Mx, bank: ExpertBank, offsets: torch.Tensor, perm, top_k: int, n_rows: int):
+def _groups(a: Mx, bank: ExpertBank, offsets: torch.Tensor, perm, top_k: int, n_rows: int, stream, device: int) -> int:
     _dev(offsets, torch.int32, "offsets")
     if offsets.numel() != bank.n_experts + 1:
         raise ValueError("offsets must have n_experts + 1 entries")
+    devices = [device, a.device, offsets.get_device()]
     if perm is not None:
         _dev(perm, torch.int32, "perm")
         if perm.numel() != n_rows:
             raise ValueError("perm must have an entry a row")
+        devices.append(perm.get_device())
     elif a.rows < n_rows:
         raise ValueError("without perm, a must have a row for each row of the output")
     if top_k < 1:
         raise ValueError("top_k must be positive")
-    _here(a.codes, offsets, perm, getattr(bank, "_keep", None))
+    keep = getattr(bank, "_keep", None)
+    if keep is not None:
+        devices.append(keep.get_device())
+    return _launch_stream(stream, *devices)
 
 
 def k3g_mx_grouped_matmul(y: torch.Tensor, a: Mx, bank: ExpertBank, tensor: int, offsets: torch.Tensor,
@@ -588,14 +618,13 @@ def k3g_mx_grouped_matmul(y: torch.Tensor, a: Mx, bank: ExpertBank, tensor: int,
     if tensor not in (W1, W3, W2):
         raise ValueError("tensor must be W1, W3 or W2")
     rows, cols = (bank.latent, bank.inter) if tensor == W2 else (bank.inter, bank.latent)
-    ld = _rows(y, "y")
-    if y.shape[1] != rows or a.n_in != cols:
+    ld = _rows(y, "y", -1, rows)
+    if a.n_in != cols:
         raise ValueError("shape mismatch")
-    _groups(a, bank, offsets, perm, top_k, y.shape[0])
-    _here(y)
+    st = _groups(a, bank, offsets, perm, top_k, y.shape[0], stream, y.get_device())
     _check("k3g_mx_grouped_matmul", lib().k3g_mx_grouped_matmul(
-        y.data_ptr(), _TYPES[y.dtype], ld, C.byref(a.struct), C.byref(bank), tensor, offsets.data_ptr(),
-        None if perm is None else perm.data_ptr(), top_k, y.shape[0], _stream(stream)))
+        y.data_ptr(), _TYPES[y.dtype], ld, a._ref, C.byref(bank), tensor, offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), top_k, y.shape[0], st))
     return y
 
 
@@ -607,11 +636,10 @@ def k3g_mx_grouped_glu(h: Mx, a: Mx, bank: ExpertBank, offsets: torch.Tensor, pe
     _mx_arg(a, "a")
     if h.n_in != bank.inter or a.n_in != bank.latent:
         raise ValueError("shape mismatch")
-    _groups(a, bank, offsets, perm, top_k, h.rows)
-    _here(h.codes)
+    st = _groups(a, bank, offsets, perm, top_k, h.rows, stream, h.device)
     _check("k3g_mx_grouped_glu", lib().k3g_mx_grouped_glu(
-        C.byref(h.struct), C.byref(a.struct), C.byref(bank), offsets.data_ptr(),
-        None if perm is None else perm.data_ptr(), top_k, h.rows, _stream(stream)))
+        h._ref, a._ref, C.byref(bank), offsets.data_ptr(), None if perm is None else perm.data_ptr(), top_k, h.rows,
+        st))
     return h
 
 

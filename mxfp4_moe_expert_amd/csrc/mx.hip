@@ -93,6 +93,23 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(typename Elem<TYPE>:
     store_n<TYPE, 8>(y + row * stride + g * kGroup + 8 * j, v);
 }
 
+// v * (hi + lo) * g: `near` to the nearest fp32, `odd` cut towards zero with the
+// last bit set where anything was cut off. A second rounding of `odd` to fewer
+// bits (a code, a bf16) is then the rounding of the product itself, never that
+// of a tie that the first rounding made.
+struct Scaled {
+    float near, odd;
+};
+__device__ inline Scaled scaled(float v, float hi, float lo, float g) {
+    const float a = v * hi, a_lo = __builtin_fmaf(v, lo, __builtin_fmaf(v, hi, -a));
+    const float b = a * g, b_lo = __builtin_fmaf(a_lo, g, __builtin_fmaf(a, g, -b));
+    const float s = b + b_lo, t = b_lo - (s - b);  // s + t = b + b_lo
+    if (!(__builtin_fabsf(b) < __builtin_inff()) || !(__builtin_fabsf(s) < __builtin_inff())) return {b, b};
+    uint32_t u = __builtin_bit_cast(uint32_t, s);
+    if (t != 0.0f && s != 0.0f) u = ((t < 0.0f) != (s < 0.0f) ? u - 1 : u) | 1u;  // |s| above the product: one down
+    return {s, __builtin_bit_cast(float, u)};
+}
+
 // One workgroup a row, its entries in registers between the sum of squares and
 // the scaling: thread c holds entries 8(c + k * threads) .. + 7, k < NC, so a
 // quad of lanes holds a group and a wavefront 2 KB of fp32.
@@ -109,7 +126,7 @@ struct NormArgs {
 template <int TYPE, int FMT, int NC>  // FMT -1: no quantised output
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
     typedef typename Elem<TYPE>::T T;
-    __shared__ float part[16];
+    __shared__ double part[16];
     const int64_t row = blockIdx.x;
     const int in = a.in, nt = blockDim.x;
     const T *x = (const T *)a.x + row * a.xs;
@@ -134,12 +151,16 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[k][i], v[k][i], ss);
     }
-    ss = wave_sum(ss);
-    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = ss;
+    // The row's scale in 64 bits from here on, and each n to about 48 (a product of two
+    // pairs of floats): an n that fp32 had rounded might cross the border between two codes.
+    // 64 wavefront sums and one root a row cost nothing next to the row's bytes.
+    const double wave_ss = wave_sum_f64((double)ss);
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = wave_ss;
     __syncthreads();
-    float tot = 0.f;
+    double tot = 0.;
     for (int w = 0; w < nt / kWave; ++w) tot += part[w];
-    const float inv = 1.0f / sqrtf(tot / (float)in + a.eps);
+    const double inv = 1.0 / sqrt(tot / in + (double)a.eps);
+    const float inv_hi = (float)inv, inv_lo = (float)(inv - (double)inv_hi);
     const int G = in / kGroup;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
@@ -148,9 +169,14 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
         if (live) {
             float gm[8];
             load_n<K3G_F32, 8>(gm, a.gamma + c);
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * inv * gm[i];
-            if (a.y) store_n<TYPE, 8>((T *)a.y + row * a.ys + c, v[k]);
+            for (int i = 0; i < 8; ++i) {
+                const Scaled n = scaled(v[k][i], inv_hi, inv_lo, gm[i]);
+                v[k][i] = n.odd;
+                y[i] = TYPE == K3G_F32 ? n.near : n.odd;
+            }
+            if (a.y) store_n<TYPE, 8>((T *)a.y + row * a.ys + c, y);
         }
         if constexpr (FMT >= 0)
             quantize_quad<FMT>(v[k], a.codes + (row * G + c / kGroup) * (FMT == K3G_MXFP4 ? 16 : 32),

@@ -248,13 +248,8 @@ struct Items {
     }
 };
 
-// The activations' row behind row p of y.
-__device__ inline int source_row(const MmArgs &a, int p) {
-    if (!a.perm) return p;
-    const int s = a.perm[p] / a.top_k;
-    return min(max(s, 0), a.a_rows - 1);
-}
-
-int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st);  // mxmm_tile.hip
+// mxmm_tile.hip: the tiled kernels, and whether a dense product has enough of their smallest tiles to fill the chip
+int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st);
+bool tile_fills(const MmArgs &a);
 
 }  // namespace k3g

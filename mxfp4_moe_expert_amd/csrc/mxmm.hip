@@ -15,39 +15,19 @@
 // and its scale made finite: it adds exactly nothing.
 #include "mxmm.h"
 
-#ifndef K3G_STREAM_WGS
-#define K3G_STREAM_WGS 4
-#endif
-#ifndef K3G_NT1
-#define K3G_NT1 16
-#endif
-#ifndef K3G_NT2
-#define K3G_NT2 32
-#endif
-#ifndef K3G_NT4
-#define K3G_NT4 256
-#endif
-
 namespace k3g {
 
 // ---- few tokens: the weights streamed once -----------------------------------------
 //
-// A workgroup takes up to 16 NT tokens (of one expert) and 32 outputs (GLU: 32
-// rows of w1 and the same 32 of w3), each wavefront four steps of 128 entries at
-// a time: their weights and scales are all in flight before the first product
-// (16 KB a wavefront in the GLU). The wavefronts' sums meet in LDS and are added
-// in wavefront order. Four consecutive lanes load 64 contiguous bytes of a row
-// (the L2 serves that several times faster than 16 rows in consecutive lanes) and
-// a permutation brings them into operand order.
+// A dense product of so few tokens that tiles of 128 rows would leave most CUs
+// idle: a workgroup takes 16 NT tokens and 32 outputs and splits the rows'
+// length, each wavefront four steps of 128 entries at a time: their weights and
+// scales (8 KB) are all in flight before the first product. The wavefronts' sums
+// meet in LDS and are added in wavefront order. Four consecutive lanes load 64
+// contiguous bytes of a row (the L2 serves that several times faster than 16 rows
+// in consecutive lanes) and a permutation brings them into operand order.
 constexpr int kSteps = 4;       // steps a wavefront loads together
 constexpr int kStreamWaves = 8;  // most wavefronts of a workgroup
-
-template <int AF, int MODE_, int NT_>
-struct Stream {
-    static constexpr int MODE = MODE_, NT = NT_, TILES = MODE == GLU ? 4 : 2, BN = 16 * NT, OUT = 32;
-    static constexpr int part(int waves) { return waves * TILES * NT * kWave * 16; }
-    static constexpr int lds(int waves, int E) { return part(waves) + (MODE == DENSE ? 0 : 4 * (E + 1) + 64); }
-};
 
 // Sixteen scale bytes of a row from group g on (255 past the row's end).
 __device__ inline uint4 scales16(const uint8_t *row, int g, int G) {
@@ -64,9 +44,9 @@ __device__ inline uint4 scales16(const uint8_t *row, int g, int G) {
 }
 __device__ inline uint32_t dword(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <int AF, class C>
+template <int AF, int NT>
 __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs a) {
-    constexpr int TILES = C::TILES, NT = C::NT, AH = AF == K3G_MXFP4 ? 1 : 2;
+    constexpr int TILES = 2, AH = AF == K3G_MXFP4 ? 1 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int waves = blockDim.x / kWave;
     float4_t *part = (float4_t *)lds;  // [wave][tile][token tile][lane]
@@ -76,15 +56,19 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
     const int psrc = 4 * (4 * r + q);
     const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
     const int S = (a.G + 3) / 4;
-    Items<C::MODE, C::BN, C::OUT> items(a, (int32_t *)(lds + C::part(waves)), blockDim.x);
+    Items<DENSE, 16 * NT, 32> items(a, nullptr, blockDim.x);
     Item it;
     while (items.next(it)) {
         const uint8_t *wc[TILES], *wsc[TILES], *ac[NT], *asc[NT];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int64_t first = it.e * a.stride;
-            wc[t] = a.w[t >> 1] + first + (int64_t)min(it.m0 + pair_row(lr, t & 1), a.rows - 1) * w_pitch;
-            wsc[t] = a.ws[t >> 1] + first + (int64_t)min(it.m0 + pair_row(r, t & 1), a.rows - 1) * a.G;
+            wc[t] = a.w[0] + (int64_t)min(it.m0 + pair_row(lr, t), a.rows - 1) * w_pitch;
+            wsc[t] = a.ws[0] + (int64_t)min(it.m0 + pair_row(r, t), a.rows - 1) * a.G;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            ac[j] = a.a_codes + (int64_t)(it.p + min(16 * j + lr, it.n_tok - 1)) * a_pitch;
+            asc[j] = a.a_scales + (int64_t)(it.p + min(16 * j + r, it.n_tok - 1)) * a.G;
         }
         float4_t acc[TILES][NT];
 #pragma unroll
@@ -92,7 +76,6 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
         const int nf = (it.n_tok + 15) / 16;  // token tiles with tokens
-        bool first = true;
         for (int s0 = kSteps * wave; s0 < S; s0 += kSteps * waves) {
             uint4 w[kSteps][TILES], sw[TILES];
 #pragma unroll
@@ -102,16 +85,6 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
 #pragma unroll
                 for (int t = 0; t < TILES; ++t)
                     w[i][t] = load16(wc[t] + 16 * (int64_t)min(4 * (s0 + i) + lq, a.G - 1));
-            if (first) {  // (behind the first loads of the weights)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int64_t load = source_row(a, it.p + min(16 * j + lr, it.n_tok - 1));
-                    const int64_t row = source_row(a, it.p + min(16 * j + r, it.n_tok - 1));
-                    ac[j] = a.a_codes + load * a_pitch;
-                    asc[j] = a.a_scales + row * a.G;
-                }
-                first = false;
-            }
             uint4 sa[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) sa[j] = scales16(asc[j], 4 * s0, a.G);
@@ -175,56 +148,36 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
             }
             const bool live = 16 * j + r < it.n_tok;
             const int64_t token = it.p + 16 * j + r;
-            if constexpr (C::MODE == GLU) {
-                float4_t h[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[t][i] = situ(s[t][i], s[2 + t][i]);
-                // (a.rows is a multiple of 32)
-                if (a.h_format == K3G_MXFP4)
-                    store_h<K3G_MXFP4>(a, token, it.m0 / kGroup, h[0], h[1], live);
-                else
-                    store_h<K3G_MXFP8>(a, token, it.m0 / kGroup, h[0], h[1], live);
-            } else {
-                const int row = it.m0 + 8 * q;
-                if (live) with_store(a, [&](auto store) { store(token * a.ys + row, a.rows - row, s[0], s[1]); });
-            }
+            const int row = it.m0 + 8 * q;
+            if (live) with_store(a, [&](auto store) { store(token * a.ys + row, a.rows - row, s[0], s[1]); });
         }
         __syncthreads();  // part is read before the next item writes it
     }
 }
 
-template <int AF, class C>
+template <int AF, int NT>
 int launch_stream(const MmArgs &a, hipStream_t st) {
     const int chunks = ((a.G + 3) / 4 + kSteps - 1) / kSteps;
     const int waves = chunks < kStreamWaves ? chunks : kStreamWaves;
-    const int bytes = C::lds(waves, a.E);
-    if (bytes > 65536 && hipFuncSetAttribute((const void *)mx_stream_kernel<AF, C>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
-        return K3G_EHIP;
-    const int64_t n_rb = (a.rows + C::OUT - 1) / C::OUT;
-    const int64_t tiles = C::MODE == DENSE ? ((int64_t)a.T + C::BN - 1) / C::BN
-                                           : a.T / C::BN + (a.E < a.T ? a.E : a.T);
-    const int64_t items = tiles * n_rb, most = 256 * K3G_STREAM_WGS, grid = items < most ? (items + 7) / 8 * 8 : most;
-    mx_stream_kernel<AF, C><<<(unsigned)grid, waves * kWave, bytes, st>>>(a);
+    const int64_t items = ((int64_t)a.rows + 31) / 32 * (((int64_t)a.T + 16 * NT - 1) / (16 * NT));
+    const int64_t most = 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
+    mx_stream_kernel<AF, NT><<<(unsigned)grid, waves * kWave, waves * 2 * NT * kWave * 16, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
-// Which kernel: rules on the rows (of the whole call, or an expert on average).
-template <int AF, int MODE>
-int launch_product(const MmArgs &a, hipStream_t st) {
-    if constexpr (MODE == DENSE) {
-        if (a.T <= K3G_NT1) return launch_stream<AF, Stream<AF, MODE, 1>>(a, st);
-        if (a.T <= K3G_NT2) return launch_stream<AF, Stream<AF, MODE, 2>>(a, st);
-        if (a.T <= K3G_NT4) return launch_stream<AF, Stream<AF, MODE, 4>>(a, st);
-    }
-    return launch_tile(a, MODE, AF, st);
+// Grouped products and dense ones with enough tiles of 128 x 32 run tiled (256
+// tokens at 7168 -> 3584: 20 us, here 19; 160 at 3584 -> 7168: 13, here 18; 96 at
+// 7168 -> 3584: 20, here 10).
+template <int AF>
+int launch_product(const MmArgs &a, int mode, hipStream_t st) {
+    if (mode != DENSE || tile_fills(a)) return launch_tile(a, mode, AF, st);
+    if (a.T <= 16) return launch_stream<AF, 1>(a, st);
+    if (a.T <= 32) return launch_stream<AF, 2>(a, st);
+    return launch_stream<AF, 4>(a, st);
 }
 
-template <int MODE>
-int launch_any(const MmArgs &a, int af, hipStream_t st) {
-    return af == K3G_MXFP4 ? launch_product<K3G_MXFP4, MODE>(a, st) : launch_product<K3G_MXFP8, MODE>(a, st);
+int launch_any(const MmArgs &a, int mode, int af, hipStream_t st) {
+    return af == K3G_MXFP4 ? launch_product<K3G_MXFP4>(a, mode, st) : launch_product<K3G_MXFP8>(a, mode, st);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -252,6 +205,7 @@ int bank_ok(const k3g_expert_bank *b) {
 int use_tensor(MmArgs *a, int slot, const k3g_expert_bank &b, int t, Span *covers) {
     const Tensor d = bank_tensor(b, t);
     const uint8_t *w = b.base + b.off[d.p], *s = b.base + b.off[d.s];
+    if (b.stride < 0) return K3G_EINVAL;
     if (!mx_aligned(w, 16) || b.stride % 16) return K3G_EALIGN;
     a->w[slot] = w;
     a->ws[slot] = s;
@@ -307,7 +261,7 @@ int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const 
     m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, w->rows);
     m.T = a->rows, m.rows = w->rows, m.in = a->in, m.G = a->in / kGroup;
     m.odd = odd_scales(m);
-    return launch_any<DENSE>(m, a->format, (hipStream_t)stream);
+    return launch_any(m, DENSE, a->format, (hipStream_t)stream);
 }
 
 int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_expert_bank *bank,
@@ -335,7 +289,7 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
     m.y = y, m.ys = y_stride, m.y_type = y_type, m.y_vec = y_vec(y, y_type, y_stride, d.rows);
     m.T = n_rows, m.rows = d.rows, m.in = d.in, m.G = d.in / kGroup;
     m.odd = odd_scales(m);
-    return launch_any<GROUPED>(m, a->format, (hipStream_t)stream);
+    return launch_any(m, GROUPED, a->format, (hipStream_t)stream);
 }
 
 int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *bank, const int32_t *offsets,
@@ -367,7 +321,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
     m.h_codes = h->codes, m.h_scales = h->scales, m.h_format = h->format;
     m.T = n_rows, m.rows = bank->inter, m.in = bank->latent, m.G = bank->latent / kGroup;
     m.odd = odd_scales(m);
-    return launch_any<GLU>(m, a->format, (hipStream_t)stream);
+    return launch_any(m, GLU, a->format, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -462,41 +462,59 @@ int launch(const MmArgs &a, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
-#ifndef K3G_TILE_BIG
-#define K3G_TILE_BIG 2, 4, 8, 4, 4
-#endif
-#ifndef K3G_TILE_MID
-#define K3G_TILE_MID 4, 2, 4, 4, 4
-#endif
-#ifndef K3G_TILE_LOW
-#define K3G_TILE_LOW 2, 2, 4, 2, 3
-#endif
+// ---- which tile ------------------------------------------------------------------------
+//
+// Dense: the largest tile that still gives kFill items, about two thirds of the
+// chip's 256 CUs (an item costs its row's length in stages whatever its size, so
+// idle CUs cost more than the larger tile's better reuse gains). Measured in us
+// at 7168 -> 3584 (MXFP4), items in brackets: 512 tokens 128 x 128 26 (112),
+// 128 x 64 23 (224); 1024 tokens 256 x 128 38 (112), 128 x 128 28 (224), 128 x 64
+// 31 (448); 2048 tokens 256 x 128 40 (224), 128 x 128 43 (448). An e4m3 tile of
+// 128 x 128 has room for two stages on two workgroups only and loses to both its
+// neighbours (1024 tokens: 66 against 53 and 79).
+constexpr int kFill = 160;
 
-#ifndef K3G_TILE_MID8
-#define K3G_TILE_MID8 2, 4, 8, 2, 3
-#endif
-#ifndef K3G_LOW_PER
-#define K3G_LOW_PER 32
-#endif
-#ifndef K3G_TILE_TINY
-#define K3G_TILE_TINY 2, 2, 4, 1, 4
-#endif
-#ifndef K3G_TINY_PER
-#define K3G_TINY_PER 8
-#endif
+// Grouped: by the rows an expert has on average over the whole bank (what the
+// host knows; a routing leaves some experts empty, so a group is larger). Up to
+// 8 rows the weights' bytes are all that counts: 32 tokens a tile, three
+// workgroups a CU. Measured at 896 experts (skewed: 290-350 with rows): 8192
+// rows 128 x 64 371 us, 256 x 128 382; 16384 rows 510 and 453.
+template <int AF, int MODE, bool ODD>
+struct Tiles {
+    typedef Tile<AF, MODE, 2, 4, 8, 4, 4, ODD> T256x256;  // e2m1
+    typedef Tile<AF, MODE, 4, 2, 4, 4, 4, ODD> T256x128;  // e2m1
+    typedef Tile<AF, MODE, 2, 4, 8, 2, 3, ODD> E256x128;  // e4m3: a token tile is cut once for eight weight tiles
+    typedef Tile<AF, MODE, 2, 2, 4, 4, 3, ODD> T128x128;  // e2m1
+    typedef Tile<AF, MODE, 2, 2, 4, 2, 3, ODD> T128x64;
+    typedef Tile<AF, MODE, 2, 2, 4, 1, 4, ODD> T128x32;
+};
+
+template <class C>
+bool fills(const MmArgs &a) {
+    return ((int64_t)a.rows + C::OUT - 1) / C::OUT * (((int64_t)a.T + C::BN - 1) / C::BN) >= kFill;
+}
+
 template <int AF, int MODE, bool ODD>
 int launch_mode(const MmArgs &a, hipStream_t st) {
-    if constexpr (MODE != DENSE) {
-        if (a.T <= K3G_TINY_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_TINY, ODD>>(a, st);
+    typedef Tiles<AF, MODE, ODD> Ts;
+    if constexpr (MODE == DENSE) {
+        if constexpr (AF == K3G_MXFP4) {
+            if (fills<typename Ts::T256x256>(a)) return launch<AF, typename Ts::T256x256>(a, st);
+            if (fills<typename Ts::T256x128>(a)) return launch<AF, typename Ts::T256x128>(a, st);
+            if (fills<typename Ts::T128x128>(a)) return launch<AF, typename Ts::T128x128>(a, st);
+        } else {
+            if (fills<typename Ts::E256x128>(a)) return launch<AF, typename Ts::E256x128>(a, st);
+        }
+        if (fills<typename Ts::T128x64>(a)) return launch<AF, typename Ts::T128x64>(a, st);
+        return launch<AF, typename Ts::T128x32>(a, st);
+    } else {
+        if (a.T <= 8 * (int64_t)a.E) return launch<AF, typename Ts::T128x32>(a, st);
+        if (a.T <= 16 * (int64_t)a.E) return launch<AF, typename Ts::T128x64>(a, st);
+        if constexpr (AF == K3G_MXFP4)
+            return launch<AF, typename Ts::T256x128>(a, st);
+        else
+            return launch<AF, typename Ts::E256x128>(a, st);
     }
-    if (MODE == DENSE ? a.T <= 64 : a.T <= K3G_LOW_PER * a.E) return launch<AF, Tile<AF, MODE, K3G_TILE_LOW, ODD>>(a, st);
-    if constexpr (AF == K3G_MXFP4 && MODE == DENSE) {
-        if ( (int64_t)a.T * a.rows >= 128 * 65536) return launch<AF, Tile<AF, MODE, K3G_TILE_BIG, ODD>>(a, st);
-    }
-    if constexpr (AF == K3G_MXFP8)
-        return launch<AF, Tile<AF, MODE, K3G_TILE_MID8, ODD>>(a, st);
-    else
-        return launch<AF, Tile<AF, MODE, K3G_TILE_MID, ODD>>(a, st);
 }
 
 template <int AF, bool ODD>
@@ -506,8 +524,11 @@ int launch_af(const MmArgs &a, int mode, hipStream_t st) {
                              : launch_mode<AF, GLU, ODD>(a, st);
 }
 
+bool tile_fills(const MmArgs &a) { return fills<Tiles<K3G_MXFP4, DENSE, false>::T128x32>(a); }
+
 int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st) {
-    if (a.odd) return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, true>(a, mode, st) : launch_af<K3G_MXFP8, true>(a, mode, st);
+    if (a.odd)
+        return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, true>(a, mode, st) : launch_af<K3G_MXFP8, true>(a, mode, st);
     return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, false>(a, mode, st) : launch_af<K3G_MXFP8, false>(a, mode, st);
 }
 
