@@ -93,21 +93,21 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(typename Elem<TYPE>:
     store_n<TYPE, 8>(y + row * stride + g * kGroup + 8 * j, v);
 }
 
-// v * (hi + lo) * g: `near` to the nearest fp32, `odd` cut towards zero with the
-// last bit set where anything was cut off. A second rounding of `odd` to fewer
-// bits (a code, a bf16) is then the rounding of the product itself, never that
-// of a tie that the first rounding made.
+// v * (hi + lo) * g as p + lo to about 48 bits: `near` is p, `odd` is cut
+// towards zero with the last bit set where anything was cut off. A second
+// rounding of `odd` to fewer bits (a code, a bf16) is then the rounding of the
+// product itself, never that of a tie that the first rounding made.
 struct Scaled {
     float near, odd;
 };
 __device__ inline Scaled scaled(float v, float hi, float lo, float g) {
-    const float a = v * hi, a_lo = __builtin_fmaf(v, lo, __builtin_fmaf(v, hi, -a));
-    const float b = a * g, b_lo = __builtin_fmaf(a_lo, g, __builtin_fmaf(a, g, -b));
-    const float s = b + b_lo, t = b_lo - (s - b);  // s + t = b + b_lo
-    if (!(__builtin_fabsf(b) < __builtin_inff()) || !(__builtin_fabsf(s) < __builtin_inff())) return {b, b};
-    uint32_t u = __builtin_bit_cast(uint32_t, s);
-    if (t != 0.0f && s != 0.0f) u = ((t < 0.0f) != (s < 0.0f) ? u - 1 : u) | 1u;  // |s| above the product: one down
-    return {s, __builtin_bit_cast(float, u)};
+    const float s = g * hi, s_lo = __builtin_fmaf(g, lo, __builtin_fmaf(g, hi, -s));
+    const float p = v * s, p_lo = __builtin_fmaf(v, s_lo, __builtin_fmaf(v, s, -p));
+    // what was cut off has p's sign: p with its last bit set; else one below p in magnitude
+    const uint32_t u = __builtin_bit_cast(uint32_t, p), w = __builtin_bit_cast(uint32_t, p_lo);
+    const uint32_t odd = (u + (uint32_t)((int32_t)(u ^ w) >> 31)) | 1u;
+    // 0x198: a number other than zero (of an infinite or NaN p, p_lo is a NaN)
+    return {p, __builtin_amdgcn_classf(p_lo, 0x198) ? __builtin_bit_cast(float, odd) : p};
 }
 
 // One workgroup a row, its entries in registers between the sum of squares and
@@ -121,6 +121,7 @@ struct NormArgs {
     const float *gamma;
     float eps;
     int in;
+    double inv_in;  // 1 / in
 };
 
 template <int TYPE, int FMT, int NC>  // FMT -1: no quantised output
@@ -159,7 +160,10 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
     __syncthreads();
     double tot = 0.;
     for (int w = 0; w < nt / kWave; ++w) tot += part[w];
-    const double inv = 1.0 / sqrt(tot / in + (double)a.eps);
+    // 1/sqrt by the fp32 instruction and one Newton step in 64 bits (an error of 1e-7
+    // becomes 1e-14); a mean of zero or infinity keeps the instruction's answer.
+    const double m = tot * a.inv_in + (double)a.eps, r0 = (double)__builtin_amdgcn_rsqf((float)m);
+    const double e = __builtin_fma(-m * r0, r0, 1.0), inv = e == e ? __builtin_fma(0.5 * r0, e, r0) : r0;
     const float inv_hi = (float)inv, inv_lo = (float)(inv - (double)inv_hi);
     const int G = in / kGroup;
 #pragma unroll
@@ -184,10 +188,13 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
     }
 }
 
+// Threads a row: with rows to fill the chip many times over, up to 512 (several
+// workgroups on a CU hide each other's waits: 8192 bf16 rows of 7168 in 81 us, 5.1 TB/s;
+// 84 with 896 threads a row, 88 with 256); with few rows, eight entries a thread.
 template <int TYPE, int FMT>
 int launch_norm(const NormArgs &a, int n_rows, hipStream_t st) {
-    const int chunks = a.in / 8;
-    const int nc = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
+    const int chunks = a.in / 8, wide = n_rows >= 1024 ? 512 : 1024;
+    const int nc = chunks <= wide ? 1 : chunks <= 2 * wide ? 2 : chunks <= 4 * wide ? 4 : 8;
     const int nt = ((chunks + nc - 1) / nc + kWave - 1) / kWave * kWave;
     if (nc == 1)
         add_rmsnorm_kernel<TYPE, FMT, 1><<<n_rows, nt, 0, st>>>(a);
@@ -302,7 +309,8 @@ int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, co
     }
     K3G_TRY(device_ok());
     const NormArgs a = {y,        sum,      x,        r,          y_stride,  sum_stride, x_stride,
-                        r_stride, q ? q->codes : nullptr, q ? q->scales : nullptr, gamma, eps, in};
+                        r_stride, q ? q->codes : nullptr, q ? q->scales : nullptr, gamma, eps, in,
+                        1.0 / in};
     const int fmt = q ? q->format : -1;
     hipStream_t st = (hipStream_t)stream;
     return type == K3G_F32    ? norm_fmt<K3G_F32>(a, fmt, n_rows, st)

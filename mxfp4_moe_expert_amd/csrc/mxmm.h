@@ -95,6 +95,19 @@ __device__ inline void store8(void *y, int64_t at, int n, const float4_t &lo, co
     }
 }
 
+// Four consecutive outputs, where a tile has no partner.
+__device__ inline void store4(const MmArgs &a, int64_t at, int n, const float4_t &v) {
+    for (int i = 0; i < 4 && i < n; ++i) {
+        const float x = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+        if (a.y_type == K3G_F32)
+            ((float *)a.y)[at + i] = x;
+        else if (a.y_type == K3G_BF16)
+            ((__bf16 *)a.y)[at + i] = (__bf16)x;
+        else
+            ((_Float16 *)a.y)[at + i] = (_Float16)x;
+    }
+}
+
 // f(store) with store = store8 for y's type and alignment (uniform).
 template <class F>
 __device__ inline void with_store(const MmArgs &a, F f) {

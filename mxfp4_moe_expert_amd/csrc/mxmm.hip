@@ -20,14 +20,14 @@ namespace k3g {
 // ---- few tokens: the weights streamed once -----------------------------------------
 //
 // A dense product of so few tokens that tiles of 128 rows would leave most CUs
-// idle: a workgroup takes 16 NT tokens and 32 outputs and splits the rows'
+// idle: a workgroup takes 16 NT tokens and 16 TILES outputs and splits the rows'
 // length, each wavefront four steps of 128 entries at a time: their weights and
-// scales (8 KB) are all in flight before the first product. The wavefronts' sums
+// scales (4 KB a tile) are all in flight before the first product. The wavefronts' sums
 // meet in LDS and are added in wavefront order. Four consecutive lanes load 64
 // contiguous bytes of a row (the L2 serves that several times faster than 16 rows
 // in consecutive lanes) and a permutation brings them into operand order.
 constexpr int kSteps = 4;       // steps a wavefront loads together
-constexpr int kStreamWaves = 8;  // most wavefronts of a workgroup
+constexpr int stream_waves(int nt) { return nt == 1 ? 16 : 8; }  // most wavefronts of a workgroup
 
 // Sixteen scale bytes of a row from group g on (255 past the row's end).
 __device__ inline uint4 scales16(const uint8_t *row, int g, int G) {
@@ -44,9 +44,9 @@ __device__ inline uint4 scales16(const uint8_t *row, int g, int G) {
 }
 __device__ inline uint32_t dword(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <int AF, int NT>
-__global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs a) {
-    constexpr int TILES = 2, AH = AF == K3G_MXFP4 ? 1 : 2;
+template <int AF, int NT, int TILES>
+__global__ __launch_bounds__(stream_waves(NT) * kWave) void mx_stream_kernel(MmArgs a) {
+    constexpr int AH = AF == K3G_MXFP4 ? 1 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int waves = blockDim.x / kWave;
     float4_t *part = (float4_t *)lds;  // [wave][tile][token tile][lane]
@@ -56,14 +56,14 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
     const int psrc = 4 * (4 * r + q);
     const int w_pitch = a.in / 2, a_pitch = AF == K3G_MXFP4 ? a.in / 2 : a.in;
     const int S = (a.G + 3) / 4;
-    Items<DENSE, 16 * NT, 32> items(a, nullptr, blockDim.x);
+    Items<DENSE, 16 * NT, 16 * TILES> items(a, nullptr, blockDim.x);
     Item it;
     while (items.next(it)) {
         const uint8_t *wc[TILES], *wsc[TILES], *ac[NT], *asc[NT];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            wc[t] = a.w[0] + (int64_t)min(it.m0 + pair_row(lr, t), a.rows - 1) * w_pitch;
-            wsc[t] = a.ws[0] + (int64_t)min(it.m0 + pair_row(r, t), a.rows - 1) * a.G;
+            wc[t] = a.w[0] + (int64_t)min(it.m0 + (TILES == 2 ? pair_row(lr, t) : lr), a.rows - 1) * w_pitch;
+            wsc[t] = a.ws[0] + (int64_t)min(it.m0 + (TILES == 2 ? pair_row(r, t) : r), a.rows - 1) * a.G;
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -148,20 +148,24 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void mx_stream_kernel(MmArgs 
             }
             const bool live = 16 * j + r < it.n_tok;
             const int64_t token = it.p + 16 * j + r;
-            const int row = it.m0 + 8 * q;
-            if (live) with_store(a, [&](auto store) { store(token * a.ys + row, a.rows - row, s[0], s[1]); });
+            const int row = it.m0 + 4 * TILES * q;
+            if constexpr (TILES == 2) {
+                if (live) with_store(a, [&](auto store) { store(token * a.ys + row, a.rows - row, s[0], s[1]); });
+            } else {
+                if (live) store4(a, token * a.ys + row, a.rows - row, s[0]);
+            }
         }
         __syncthreads();  // part is read before the next item writes it
     }
 }
 
-template <int AF, int NT>
+template <int AF, int NT, int TILES>
 int launch_stream(const MmArgs &a, hipStream_t st) {
     const int chunks = ((a.G + 3) / 4 + kSteps - 1) / kSteps;
-    const int waves = chunks < kStreamWaves ? chunks : kStreamWaves;
-    const int64_t items = ((int64_t)a.rows + 31) / 32 * (((int64_t)a.T + 16 * NT - 1) / (16 * NT));
+    const int waves = chunks < stream_waves(NT) ? chunks : stream_waves(NT);
+    const int64_t items = ((int64_t)a.rows + 16 * TILES - 1) / (16 * TILES) * (((int64_t)a.T + 16 * NT - 1) / (16 * NT));
     const int64_t most = 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
-    mx_stream_kernel<AF, NT><<<(unsigned)grid, waves * kWave, waves * 2 * NT * kWave * 16, st>>>(a);
+    mx_stream_kernel<AF, NT, TILES><<<(unsigned)grid, waves * kWave, waves * TILES * NT * kWave * 16, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
@@ -171,9 +175,10 @@ int launch_stream(const MmArgs &a, hipStream_t st) {
 template <int AF>
 int launch_product(const MmArgs &a, int mode, hipStream_t st) {
     if (mode != DENSE || tile_fills(a)) return launch_tile(a, mode, AF, st);
-    if (a.T <= 16) return launch_stream<AF, 1>(a, st);
-    if (a.T <= 32) return launch_stream<AF, 2>(a, st);
-    return launch_stream<AF, 4>(a, st);
+    // up to 16 tokens 16 outputs a workgroup, while those are not more than a few rounds of the chip
+    if (a.T <= 16) return a.rows <= 16384 ? launch_stream<AF, 1, 1>(a, st) : launch_stream<AF, 1, 2>(a, st);
+    if (a.T <= 32) return launch_stream<AF, 2, 2>(a, st);
+    return launch_stream<AF, 4, 2>(a, st);
 }
 
 int launch_any(const MmArgs &a, int mode, int af, hipStream_t st) {
