@@ -485,7 +485,7 @@ struct Tiles {
     typedef Tile<AF, MODE, 4, 2, 4, 4, 4, ODD> T256x128;  // e2m1
     typedef Tile<AF, MODE, 2, 4, 8, 2, 3, ODD> E256x128;  // e4m3: a token tile is cut once for eight weight tiles
     typedef Tile<AF, MODE, 2, 2, 4, 4, 3, ODD> T128x128;  // e2m1
-    typedef Tile<AF, MODE, 2, 2, 4, 2, 3, ODD> T128x64;
+    typedef Tile<AF, MODE, 2, 2, 4, 2, AF == K3G_MXFP4 ? 4 : 3, ODD> T128x64;
     typedef Tile<AF, MODE, 2, 2, 4, 1, 4, ODD> T128x32;
 };
 
