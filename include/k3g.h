@@ -507,7 +507,8 @@ int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, co
 /* y[t][n] = sum over 32-groups of 2^(sa-127) 2^(sw-127) sum_j a_tj w_nj for a
  * microscaled a [T][in] and an MXFP4 w [rows][in]: the block-scaled matrix
  * cores on both as they are stored, products exact, sums in fp32, rounded once
- * to y_type. y rows y_stride >= w->rows entries apart. A group with byte 255 in
+ * to y_type. y rows y_stride >= w->rows entries apart; at most 2^30 rows of a
+ * and of w. A group with byte 255 in
  * a or in w adds nothing (e4m3 NaN codes, which the quantiser does not
  * write, propagate wherever a's byte is not 255). y must overlap no input. */
 int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_mxfp4 *w, void *stream);
@@ -524,7 +525,7 @@ typedef enum { K3G_W1 = 0, K3G_W3 = 1, K3G_W2 = 2 } k3g_bank_tensor;
  * were. Preconditions (not checked on the device, but nothing out of range is
  * read or written without them): offsets ascending within [0, n_rows], perm
  * values in [0, a->rows * top_k). Without perm a->rows >= n_rows. y has n_rows
- * rows. n_experts <= 2048; with perm a->rows * in < 2^31. */
+ * rows (at most 2^30). n_experts <= 2048; with perm a->rows * in < 2^31. */
 int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_expert_bank *bank,
                           int tensor, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows,
                           void *stream);

@@ -190,6 +190,7 @@ int launch_any(const MmArgs &a, int mode, int af, hipStream_t st) {
 namespace {
 
 constexpr int kMaxExperts = 2048;
+constexpr int kMaxRows = 1 << 30;  // tiles are counted in 32 bits
 
 struct Tensor {
     int p, s, rows, in;
@@ -223,6 +224,7 @@ int use_tensor(MmArgs *a, int slot, const k3g_expert_bank &b, int t, Span *cover
 // What the two grouped calls check alike.
 int groups_ok(const k3g_mx *a, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows) {
     if (!offsets) return K3G_EINVAL;
+    if (n_rows > kMaxRows) return K3G_EUNSUPPORTED;
     if (!mx_aligned(offsets, 4) || (perm && !mx_aligned(perm, 4))) return K3G_EALIGN;
     if (!perm && a->rows < n_rows) return K3G_EINVAL;
     if (a->rows < 1) return K3G_EINVAL;
@@ -250,6 +252,7 @@ extern "C" {
 int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_mxfp4 *w, void *stream) {
     K3G_TRY(mx_ok(a));
     if (!w || w->rows < 1 || w->in != a->in || !type_ok(y_type) || y_stride < w->rows) return K3G_EINVAL;
+    if (a->rows > kMaxRows || w->rows > kMaxRows) return K3G_EUNSUPPORTED;
     if (a->rows == 0) return K3G_OK;
     if (!w->packed || !w->scales) return K3G_EINVAL;
     if (!mx_aligned(w->packed, 16)) return K3G_EALIGN;

@@ -83,6 +83,8 @@ def test_product_refusals(k3g):
                 {"w": k3g.Mxfp4(3 * M, None, 8, 64)}, {"a": mx(k3g, 2 * M, fmt=5)}, {"y": 2 * M}, {"y": 3 * M},
                 {"y": 4 * M - 64}, {"y": 2 * M + M // 2}):
         assert mm(**bad) == EINVAL, bad
+    assert mm(a=mx(k3g, 1 << 40, rows=(1 << 30) + 1, scales=1 << 45)) == UNSUPPORTED
+    assert mm(w=k3g.Mxfp4(1 << 40, 1 << 45, (1 << 30) + 1, 64), ld=1 << 31) == UNSUPPORTED
     assert mm(w=k3g.Mxfp4(3 * M + 4, 4 * M, 8, 64)) == EALIGN
     assert mm(y=M + 2) == EALIGN
     assert mm(a=mx(k3g, 0, rows=0, scales=0), y=None) == 0
@@ -111,6 +113,7 @@ def test_grouped_refusals(k3g):
                     {"k": 0}, {"n": -1}, {"perm": None}):  # no perm: a has fewer rows than the output
             assert call(**bad) == EINVAL, (call.__name__, bad)
         assert call(b=bank(k3g, E=2049)) == UNSUPPORTED
+        assert call(b=bank(k3g, stride=-16384)) == EINVAL
         assert call(b=bank(k3g, stride=bank(k3g).stride + 8)) == EALIGN
         assert call(b=bank(k3g, base=16 * M + 8)) == EALIGN
         assert call(off=4 * M + 2) == EALIGN
