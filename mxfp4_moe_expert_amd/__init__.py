@@ -445,7 +445,7 @@ class Mx:
     """A microscaled matrix (k3g_mx): codes uint8 [rows, in/2] (MXFP4) or
     [rows, in] (MXFP8), scales uint8 [rows, in/32], and their format."""
 
-    __slots__ = ("codes", "scales", "format", "rows", "n_in", "device", "struct", "_ref")
+    __slots__ = ("_codes", "_scales", "_buf", "format", "rows", "n_in", "device", "struct", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int):
         if fmt not in (MXFP4, MXFP8):
@@ -459,13 +459,27 @@ class Mx:
             raise ValueError("scales must be [rows, in/32]")
         if scales.device != codes.device:
             raise ValueError("codes and scales must be on one device")
-        self._set(codes, scales, fmt, codes.shape[0], n_in)
+        self._codes, self._scales, self._buf = codes, scales, None
+        self._set(codes.data_ptr(), scales.data_ptr(), fmt, codes.shape[0], n_in, codes.get_device())
 
-    def _set(self, codes, scales, fmt, rows, n_in):
-        self.codes, self.scales, self.format, self.rows, self.n_in = codes, scales, fmt, rows, n_in
-        self.device = codes.get_device()
-        self.struct = MxStruct(codes.data_ptr(), scales.data_ptr(), rows, n_in, fmt)
+    def _set(self, codes, scales, fmt, rows, n_in, device):
+        self.format, self.rows, self.n_in, self.device = fmt, rows, n_in, device
+        self.struct = MxStruct(codes, scales, rows, n_in, fmt)
         self._ref = C.byref(self.struct)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:  # of mx_empty: the first part of its memory
+            wide = self.n_in // 2 if self.format == MXFP4 else self.n_in
+            self._codes = self._buf.as_strided((self.rows, wide), (wide, 1))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            groups = self.n_in // GROUP
+            self._scales = self._buf.as_strided((self.rows, groups), (groups, 1), self._buf.numel() - self.rows * groups)
+        return self._scales
 
 
 def mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int) -> Mx:
@@ -477,15 +491,15 @@ def mx_empty(rows: int, n_in: int, fmt: int, device="cuda") -> Mx:
     """A microscaled matrix of that size, not initialised (codes, then scales, in one piece of memory)."""
     if fmt not in (MXFP4, MXFP8) or rows < 0 or n_in <= 0 or n_in % GROUP:
         raise ValueError("invalid microscaled shape or format")
-    wide, groups = n_in // 2 if fmt == MXFP4 else n_in, n_in // GROUP
-    at = rows * wide  # a multiple of 16
-    buf = torch.empty(at + rows * groups, dtype=torch.uint8, device=device)
-    codes = buf.as_strided((rows, wide), (wide, 1))
-    scales = buf.as_strided((rows, groups), (groups, 1), at)
-    if buf.device.type != "cuda":
-        return Mx(codes, scales, fmt)  # refused there
+    at = rows * n_in // 2 if fmt == MXFP4 else rows * n_in  # a multiple of 16
+    buf = torch.empty(at + rows * n_in // GROUP, dtype=torch.uint8, device=device)
+    dev = buf.get_device()
+    if dev < 0:
+        raise ValueError("a microscaled matrix must live on the GPU")
     q = Mx.__new__(Mx)
-    q._set(codes, scales, fmt, rows, n_in)
+    q._codes, q._scales, q._buf = None, None, buf
+    first = buf.data_ptr()
+    q._set(first, first + at, fmt, rows, n_in, dev)
     return q
 
 
@@ -554,9 +568,10 @@ def k3g_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, r: torch.T
     given (at least one of y and q). sum or y may be x or r itself. Returns (sum, y, q)."""
     ld = _rows(x, "x")
     n, n_in = x.shape
-    _dev(gamma, torch.float32, "gamma")
-    if gamma.numel() != n_in:
-        raise ValueError("gamma must have one entry a column")
+    if not isinstance(gamma, torch.Tensor) or gamma.dtype != torch.float32:
+        raise TypeError("gamma must be a float32 tensor")
+    if gamma.numel() != n_in or not gamma.is_contiguous():
+        raise ValueError("gamma must be contiguous, one entry a column")
     if y is None and q is None:
         raise ValueError("at least one of y and q")
     devices = [x.get_device(), gamma.get_device()]

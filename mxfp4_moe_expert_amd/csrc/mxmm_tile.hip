@@ -448,10 +448,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
 template <int AF, class C>
 int launch(const MmArgs &a, hipStream_t st) {
     const int bytes = C::lds(a.E);
-    // the attribute is a property of the kernel on a device: set at every
-    // launch (a host-side store), so that no state is kept here
-    if (hipFuncSetAttribute((const void *)mx_tile_kernel<AF, C>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        hipSuccess)
+    // (a host-side store, a launch's price; no state is kept here)
+    if (bytes > 65536 && hipFuncSetAttribute((const void *)mx_tile_kernel<AF, C>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return K3G_EHIP;
     const int64_t n_rb = (a.rows + C::OUT - 1) / C::OUT;
     const int64_t tiles = C::MODE == DENSE ? ((int64_t)a.T + C::BN - 1) / C::BN
