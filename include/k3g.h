@@ -483,7 +483,8 @@ typedef struct {
  * (1 for a group of zeros) and each code is x / 2^e rounded to nearest, ties to
  * the even code. A group that holds a NaN or an infinity has no value in
  * these formats: its byte is 255 and its codes are 0, so it contributes
- * nothing. x aligned to its entries. q must not overlap x. */
+ * nothing. x aligned to its entries. q must not overlap x. At most 2^30 - 64
+ * groups (K3G_EUNSUPPORTED beyond; k3g_mx_dequantize alike). */
 int k3g_mx_quantize(const k3g_mx *q, const void *x, int x_type, int64_t x_stride, void *stream);
 
 /* q -> y [rows][in] (rows y_stride entries apart): code * 2^(s-127) rounded

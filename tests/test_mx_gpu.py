@@ -589,3 +589,130 @@ def test_results_repeat_and_do_not_depend_on_neighbours(k3g):
             for o in y:
                 k3g.k3g_mx_matmul(o, a, w)
             assert torch.equal(*y), f"T={T}"
+
+
+@pytest.mark.parametrize("fmt", [None, 0, 1])
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("T,n", [(1024, 4096), (1025, 7168), (1031, 16416), (1024, 65536)])
+def test_add_rmsnorm_many_rows(k3g, T, n, ty, fmt):
+    """With 1024 rows or more a row gets fewer threads; the residual is the output's own place."""
+    print(f"norm T={T} n={n} {ty} fmt={fmt}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn(T, n, device="cuda", generator=g).to(TYPES[ty])
+    r = torch.randn(T, n, device="cuda", generator=g).to(TYPES[ty])
+    gamma = torch.rand(n, device="cuda", generator=g) + 0.5
+    s = x.double() + r.double()
+    ref = s / torch.sqrt((s * s).mean(-1, keepdim=True) + 1e-5) * gamma.double()
+    sm = torch.empty_like(x)
+    q = k3g.mx_empty(T, n, fmt) if fmt is not None else None
+    k3g.k3g_add_rmsnorm(x, gamma, 1e-5, r=r, sum=sm, y=r, q=q)
+    assert bool(((sm.double() - s).abs() <= (HALF[ty] + 2.0 ** -24) * s.abs() + 1e-7).all())
+    assert bool(((r.double() - ref).abs() <= (HALF[ty] + NORM) * ref.abs() + 2.0 ** -25).all())
+    if fmt is not None:
+        pick = [0, 1, T // 2, T - 1]
+        part = host(ref[pick])
+        mx_ref.check_quantised(host(q.codes[pick]), host(q.scales[pick]), part, NORM * np.abs(part), fmt, "norm")
+
+
+def test_add_rmsnorm_more_rows_than_one_launch(k3g):
+    """Past 2^25 rows of 64 threads the rows go out in several launches."""
+    T, n = (1 << 26) + 5, 32
+    print(f"norm T={T} n={n}", flush=True)
+    x = torch.empty(T, n, device="cuda", dtype=torch.bfloat16).normal_()
+    gamma = torch.ones(n, device="cuda")
+    y = torch.full_like(x, 9.0)
+    k3g.k3g_add_rmsnorm(x, gamma, 1e-5, y=y)
+    for at in (0, (1 << 25) - 8, 1 << 25, T - 16):
+        s = x[at:at + 16].double()
+        ref = s / torch.sqrt((s * s).mean(-1, keepdim=True) + 1e-5)
+        assert bool(((y[at:at + 16].double() - ref).abs() <= (HALF["bf16"] + NORM) * ref.abs() + 2.0 ** -25).all()), at
+
+
+def test_offsets_past_32_bits(k3g):
+    """Rows so far apart that their offsets pass 32 bits, in every dense operand, and experts 5 GiB apart."""
+    rng = np.random.default_rng(53)
+    T, n, rows, ld = 200, 256, 264, 1 << 25  # 200 rows: 6.7e9 entries
+    wide = torch.empty(T * ld, device="cuda", dtype=torch.bfloat16)
+    far = wide.as_strided((T, n), (ld, 1))
+    near = torch.from_numpy(rng.standard_normal((T, n)).astype(np.float32)).to("cuda", torch.bfloat16)
+    far.copy_(near)
+    gamma = torch.ones(n, device="cuda")
+    w = k3g.mxfp4(*[dev(b) for b in mx_ref.mx_bytes(rng, rows, n, 0)])
+    for fmt in FMTS:
+        print(f"offsets fmt={fmt}", flush=True)
+        q = [k3g.mx_empty(T, n, fmt) for _ in range(2)]
+        for o, x in zip(q, (near, far)):
+            k3g.k3g_mx_quantize(o, x)
+        assert torch.equal(q[0].codes, q[1].codes) and torch.equal(q[0].scales, q[1].scales)
+        z = [torch.empty_like(near), wide[n:].as_strided((T, n), (ld, 1))]
+        for o in z:
+            k3g.k3g_mx_dequantize(o, q[0])
+        assert torch.equal(*z)
+        for o, x in zip(z, (far, near)):  # (the gaps between far rows count as theirs: not both from one buffer)
+            k3g.k3g_add_rmsnorm(x, gamma, 1e-5, y=o)
+        assert torch.equal(*z)
+        for t in (9, 60, T):  # streamed, and with more tokens
+            a = k3g.mx(q[0].codes[:t], q[0].scales[:t], fmt)
+            y = [torch.empty(t, rows, device="cuda", dtype=torch.bfloat16), wide[2 * n:].as_strided((t, rows), (ld, 1))]
+            for o in y:
+                k3g.k3g_mx_matmul(o, a, w)
+            assert torch.equal(*y), t
+    del wide, far, z, y, o, x
+    torch.cuda.empty_cache()
+    ex = Experts(k3g, rng, 2, 64, 96)
+    stride = 5 << 30
+    apart = torch.empty(2 * stride, dtype=torch.uint8, device="cuda")
+    for e in range(2):
+        apart[e * stride:e * stride + ex.struct.stride] = ex.bank[e * ex.struct.stride:(e + 1) * ex.struct.stride]
+    b = k3g.bank_struct(apart, 2, 64, 96, list(ex.struct.off), stride)
+    P = 40
+    a = k3g.mx(*[dev(v) for v in mx_ref.mx_bytes(rng, P, 64, 1)], 1)
+    off = dev(np.array([0, 7, P], np.int32))
+    out = []
+    for s in (ex.struct, b):
+        h, y = k3g.mx_empty(P, 96, 1), torch.empty(P, 64, device="cuda")
+        k3g.k3g_mx_grouped_glu(h, a, s, off)
+        k3g.k3g_mx_grouped_matmul(y, h, s, k3g.W2, off)
+        out.append((h, y))
+    assert torch.equal(out[0][0].codes, out[1][0].codes) and torch.equal(out[0][0].scales, out[1][0].scales)
+    assert torch.equal(out[0][1], out[1][1])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_two_streams_and_repeated_sources(k3g, fmt):
+    """Calls on two streams at once share nothing; one source row may stand in many places of perm."""
+    rng = np.random.default_rng(61)
+    E, latent, inter, P = 5, 512, 288, 600
+    ex = Experts(k3g, rng, E, latent, inter)
+    off = dev(ragged(rng, E, P))
+    a = [k3g.mx(*[dev(v) for v in mx_ref.mx_bytes(rng, 9, latent, fmt)], fmt) for _ in range(2)]
+    perm = [dev(rng.integers(0, 9 * 2, P).astype(np.int32)) for _ in range(2)]
+
+    def outputs():
+        return k3g.mx_empty(P, inter, 1), torch.zeros(P, latent, device="cuda")
+
+    def step(i, o):
+        k3g.k3g_mx_grouped_glu(o[0], a[i], ex.struct, off, perm=perm[i], top_k=2)
+        k3g.k3g_mx_grouped_matmul(o[1], o[0], ex.struct, k3g.W2, off)
+
+    alone, both = [outputs() for _ in range(2)], [outputs() for _ in range(2)]
+    for i in range(2):
+        step(i, alone[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                step(i, both[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(alone[i][0].codes, both[i][0].codes) and torch.equal(alone[i][1], both[i][1])
+    av = mx_ref.values(host(a[0].codes), host(a[0].scales), fmt)
+    y = torch.zeros(P, inter, device="cuda")
+    k3g.k3g_mx_grouped_matmul(y, a[0], ex.struct, k3g.W1, off, perm=perm[0], top_k=2)
+    o, p = host(off), host(perm[0])
+    for e in range(E):
+        i = np.arange(o[e], o[e + 1])
+        if i.size:
+            ref, nrm = mx_ref.product(av[p[i] // 2], ex.w[k3g.W1][e])
+            check_product(host(y)[i].astype(np.float64), ref, nrm, "f32", f"expert {e}")

@@ -53,6 +53,12 @@ def test_quantize_refusals(k3g):
     assert L.k3g_mx_dequantize(None, 0, 64, C.byref(mx(k3g, 0, rows=0, scales=0)), None) == 0
 
 
+def test_quantize_refuses_more_groups_than_a_launch_counts(k3g):
+    for fn in (lambda q: quantize(k3g, q, x=1 << 46, t=1, ld=65536),
+               lambda q: k3g.lib().k3g_mx_dequantize(1 << 46, 1, 65536, C.byref(q), None)):
+        assert fn(mx(k3g, 1 << 40, rows=1 << 19, n=65536, scales=1 << 45)) == UNSUPPORTED
+
+
 def test_norm_refusals(k3g):
     L = k3g.lib()
 
