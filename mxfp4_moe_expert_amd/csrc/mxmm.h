@@ -245,7 +245,7 @@ struct Items {
             const int group = (int)(in_expert / (4 * n_rb)), wide = min(4, nt - group * 4);
             if (wide < 1) continue;
             const int in_group = (int)(in_expert - (int64_t)group * 4 * n_rb);
-            o.m0 = in_group / wide * OUT;
+            o.m0 = in_group / wide * OUT;  // (a table whose tiles pass 32 bits may make it negative)
             o.p = (group * 4 + in_group % wide) * BN;
             int end = a.T;
             if constexpr (MODE != DENSE) {
@@ -253,7 +253,7 @@ struct Items {
                 end = min(__builtin_amdgcn_readfirstlane(a.offsets[o.e + 1]), a.T);
             }
             o.n_tok = min(BN, end - o.p);
-            if (o.p < 0 || o.n_tok < 1 || o.m0 >= a.rows) continue;
+            if (o.p < 0 || o.n_tok < 1 || o.m0 < 0 || o.m0 >= a.rows) continue;
             item += step;
             return true;
         }
