@@ -26,6 +26,9 @@ namespace k3g {
 // meet in LDS and are added in wavefront order. Four consecutive lanes load 64
 // contiguous bytes of a row (the L2 serves that several times faster than 16 rows
 // in consecutive lanes) and a permutation brings them into operand order.
+// One MXFP8 token at 7168 -> 3584: 7.9 us for 14 MB, 61 MXFP4 tokens at 3584 ->
+// 7168: 8.3 us for 16 MB. Latency bounds both (a launch, a round of loads, the
+// sum over the wavefronts, a store); the bytes alone would take a third.
 constexpr int kSteps = 4;       // steps a wavefront loads together
 constexpr int stream_waves(int nt) { return nt == 1 ? 16 : 8; }  // most wavefronts of a workgroup
 

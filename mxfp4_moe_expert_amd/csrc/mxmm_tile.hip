@@ -21,6 +21,14 @@
 //   products of stage s, second half
 // so the matrix cores have work across the barrier, and NB - 1 stages are in
 // flight or about to be read.
+//
+// Measured, MXFP4: 4096 tokens at 7168 -> 6144 (256 x 256) 118-129 us, 2.8-3.1
+// PFLOP/s; 65536 grouped rows at 896 experts (256 x 128) 0.88 ms, 1.6 PFLOP/s, and
+// their gated up-products 1.9 ms, of which the way out (SiTU, quantising) is 17%.
+// All run at about 120 G requests of 64 bytes a second to the L2, which bounds
+// them; the matrix cores are 30% busy. 1024 grouped MXFP8 rows that meet 230
+// experts (128 x 32): 258-286 us, 4.8-5.3 TB/s of HBM, which bounds those; the 16
+// experts of one token 48 us, 3.9 TB/s (one item a workgroup: start and end show).
 #include "mxmm.h"
 
 namespace k3g {
