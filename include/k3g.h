@@ -494,9 +494,9 @@ int k3g_mx_dequantize(void *y, int y_type, int64_t y_stride, const k3g_mx *q, vo
 
 /* The residual's addition and the RMS norm of each of n_rows rows of `in`
  * entries: s = x + r in fp32 (s = x where r is null), n = s / sqrt(mean(s^2) +
- * eps) * gamma, the mean and n in fp32 from the unrounded s. Written where the
- * pointer is not null: sum = s and y = n, each rounded once to `type`, and
- * q = n quantised as k3g_mx_quantize does from the unrounded n (q->rows =
+ * eps) * gamma, the mean in 64 bits from the unrounded s and n to 2^-46 of
+ * itself. Written where the pointer is not null: sum = s and y = n, each rounded
+ * once to `type`, and q = n quantised as k3g_mx_quantize does from the unrounded n (q->rows =
  * n_rows, q->in = in). At least one of y and q. x, r, sum and y are of `type`,
  * rows x_stride, r_stride, sum_stride, y_stride entries apart (each >= in);
  * gamma fp32 [in]; eps >= 0. sum or y may be x or r itself (same pointer and

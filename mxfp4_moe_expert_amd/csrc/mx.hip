@@ -96,21 +96,25 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(typename Elem<TYPE>:
     store_n<TYPE, 8>(y + row * stride + g * kGroup + 8 * j, v);
 }
 
-// v * (hi + lo) * g as p + lo to about 48 bits: `near` is p, `odd` is cut
-// towards zero with the last bit set where anything was cut off. A second
-// rounding of `odd` to fewer bits (a code, a bf16) is then the rounding of the
-// product itself, never that of a tie that the first rounding made.
+// v * (hi + lo) * g as a sum of two floats, to about 46 bits: `near` is the nearest
+// float, `odd` the sum cut towards zero with the last bit set where anything was cut
+// off. A second rounding of `odd` to fewer bits (a code, a bf16) is then the rounding
+// of the product itself, never that of a tie that the first rounding made. (What the
+// two products leave, p_lo, can pass an ulp of p: the two are added before the cut.)
 struct Scaled {
     float near, odd;
 };
 __device__ inline Scaled scaled(float v, float hi, float lo, float g) {
+#pragma clang fp contract(off)  // p is the rounded product wherever it stands
     const float s = g * hi, s_lo = __builtin_fmaf(g, lo, __builtin_fmaf(g, hi, -s));
     const float p = v * s, p_lo = __builtin_fmaf(v, s_lo, __builtin_fmaf(v, s, -p));
-    // what was cut off has p's sign: p with its last bit set; else one below p in magnitude
-    const uint32_t u = __builtin_bit_cast(uint32_t, p), w = __builtin_bit_cast(uint32_t, p_lo);
+    // of an infinite or NaN p, p_lo is no number (0x1F8: finite)
+    const float near = __builtin_amdgcn_classf(p_lo, 0x1F8) ? p + p_lo : p, rest = p_lo - (near - p);
+    // what is left has near's sign: near with its last bit set; else one below near in magnitude
+    const uint32_t u = __builtin_bit_cast(uint32_t, near), w = __builtin_bit_cast(uint32_t, rest);
     const uint32_t odd = (u + (uint32_t)((int32_t)(u ^ w) >> 31)) | 1u;
-    // 0x198: a number other than zero (of an infinite or NaN p, p_lo is a NaN)
-    return {p, __builtin_amdgcn_classf(p_lo, 0x198) ? __builtin_bit_cast(float, odd) : p};
+    // 0x198: a number other than zero
+    return {near, __builtin_amdgcn_classf(rest, 0x198) ? __builtin_bit_cast(float, odd) : near};
 }
 
 // One workgroup a row, its entries in registers between the sum of squares and
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
     const T *x = (const T *)a.x + row * a.xs;
     const T *r = a.r ? (const T *)a.r + row * a.rs : nullptr;
     float v[NC][8];
-    float ss = 0.f;
+    double ss = 0.;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
         const int c = 8 * ((int)threadIdx.x + k * nt);
@@ -154,12 +158,12 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
             if (a.sum) store_n<TYPE, 8>((T *)a.sum + row * a.ss + c, v[k]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[k][i], v[k][i], ss);
+        for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)v[k][i], (double)v[k][i], ss);
     }
-    // The row's scale in 64 bits from here on, and each n to about 48 (a product of two
-    // pairs of floats): an n that fp32 had rounded might cross the border between two codes.
-    // 64 wavefront sums and one root a row cost nothing next to the row's bytes.
-    const double wave_ss = wave_sum_f64((double)ss);
+    // The sum of squares and the row's scale in 64 bits, and each n to about 46 (a product
+    // of two pairs of floats): an n that fp32 had rounded might cross the border between two
+    // codes. The row's bytes take longer.
+    const double wave_ss = wave_sum_f64(ss);
     if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = wave_ss;
     __syncthreads();
     double tot = 0.;
