@@ -499,8 +499,9 @@ int k3g_mx_dequantize(void *y, int y_type, int64_t y_stride, const k3g_mx *q, vo
  * once to `type`, and q = n quantised as k3g_mx_quantize does from the unrounded n (q->rows =
  * n_rows, q->in = in). At least one of y and q. x, r, sum and y are of `type`,
  * rows x_stride, r_stride, sum_stride, y_stride entries apart (each >= in);
- * gamma fp32 [in]; eps >= 0. sum or y may be x or r itself (same pointer and
- * stride); any other overlap of an output is K3G_EINVAL. in as k3g_mx. */
+ * gamma fp32 [in]; eps >= 0 (with eps = 0 a row of zeros is 0 / 0: NaN in y, byte 255
+ * in q). sum or y may be x or r itself (same pointer and stride); any other
+ * overlap of an output is K3G_EINVAL. in as k3g_mx. */
 int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, const k3g_mx *q,
                     const void *x, int64_t x_stride, const void *r, int64_t r_stride, int type,
                     const float *gamma, float eps, int n_rows, int in, void *stream);

@@ -168,11 +168,15 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
     __syncthreads();
     double tot = 0.;
     for (int w = 0; w < nt / kWave; ++w) tot += part[w];
-    // 1/sqrt by the fp32 instruction and one Newton step in 64 bits (an error of 1e-7
-    // becomes 1e-14); a mean of zero or infinity keeps the instruction's answer.
-    const double m = tot * a.inv_in + (double)a.eps, r0 = (double)__builtin_amdgcn_rsqf((float)m);
+    // 1/sqrt by the 64-bit instruction (2^-24) and one Newton step (2^-47); of a mean of zero
+    // or infinity, where the step is a NaN, the instruction's answer. It may lie past fp32's
+    // ends on either side, and so may its product with gamma: its power of two goes to the
+    // entries, which it brings to about 1, and s, hi and lo keep all their bits.
+    const double m = tot * a.inv_in + (double)a.eps, r0 = __builtin_amdgcn_rsq(m);
     const double e = __builtin_fma(-m * r0, r0, 1.0), inv = e == e ? __builtin_fma(0.5 * r0, e, r0) : r0;
-    const float inv_hi = (float)inv, inv_lo = (float)(inv - (double)inv_hi);
+    const int up = __builtin_amdgcn_frexp_exp(inv);  // inv in [2^(up-1), 2^up); of 0, infinity or NaN 0
+    const double unit = __builtin_ldexp(inv, -up);
+    const float inv_hi = (float)unit, inv_lo = (float)(unit - (double)inv_hi);
     const int G = in / kGroup;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
@@ -184,7 +188,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const Scaled n = scaled(v[k][i], inv_hi, inv_lo, gm[i]);
+                const Scaled n = scaled(__builtin_ldexpf(v[k][i], up), inv_hi, inv_lo, gm[i]);
                 v[k][i] = n.odd;
                 y[i] = TYPE == K3G_F32 ? n.near : n.odd;
             }
