@@ -147,13 +147,16 @@ __device__ inline double wave_sum_f64(double v) {
 
 // e^x to about 2 ulp: v_exp_f32 (2^t, 1 ulp) at t = x*log2(e) rounded, times
 // 1 + r*ln(2) for the part r of x*log2(e) that the rounding dropped (|r| is
-// at most 2^-17 where the result is finite, so the factor is exact enough).
+// at most 2^-17 where the result is finite, so the factor is exact enough). Of an
+// infinite or huge x, r is no such part (infinity less infinity): it is held to
+// [-1, 1], where the factor is positive, and 2^t is the result.
 __device__ inline float exp_fast(float x) {
     constexpr float kL2E = 1.44269502f;        // log2(e) rounded to fp32
     constexpr float kL2E_LO = 1.92596299e-8f;  // log2(e) - kL2E
     const float t = x * kL2E;
     const float r = __builtin_fmaf(x, kL2E_LO, __builtin_fmaf(x, kL2E, -t));
-    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, 0.693147182f, 1.0f);
+    const float part = __builtin_fminf(__builtin_fmaxf(r, -1.0f), 1.0f);  // (of a NaN r -1; a NaN x is one in 2^t)
+    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(part, 0.693147182f, 1.0f);
 }
 
 // tanh(y): below |y| = 0.3 the odd Taylor series through y^9 (the next term
