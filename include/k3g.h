@@ -458,6 +458,11 @@ int k3g_cache_query(const k3g_cache *c, k3g_cache_stats *stats, int32_t *slot_of
 
 /* ---- microscaled activations: quantiser, norm, and products with MXFP4 weights --- */
 
+/* Outputs may overlap no input and no other output (K3G_EINVAL), but for what
+ * k3g_add_rmsnorm allows. Dense operands whose rows lie equally far apart may be
+ * column slices of one buffer; next to any other operand the gaps between an
+ * operand's rows count as its own. */
+
 /* Element types of the dense tensors these calls take or write. */
 typedef enum { K3G_F32 = 0, K3G_BF16 = 1, K3G_F16 = 2 } k3g_type;
 
@@ -500,8 +505,8 @@ int k3g_mx_dequantize(void *y, int y_type, int64_t y_stride, const k3g_mx *q, vo
  * n_rows, q->in = in). At least one of y and q. x, r, sum and y are of `type`,
  * rows x_stride, r_stride, sum_stride, y_stride entries apart (each >= in);
  * gamma fp32 [in]; eps >= 0 (with eps = 0 a row of zeros is 0 / 0: NaN in y, byte 255
- * in q). sum or y may be x or r itself (same pointer and stride); any other
- * overlap of an output is K3G_EINVAL. in as k3g_mx. */
+ * in q). sum or y may be x or r itself (same pointer and stride). in as
+ * k3g_mx. */
 int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, const k3g_mx *q,
                     const void *x, int64_t x_stride, const void *r, int64_t r_stride, int type,
                     const float *gamma, float eps, int n_rows, int in, void *stream);

@@ -565,7 +565,8 @@ def k3g_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, r: torch.T
                     sum: torch.Tensor | None = None, y: torch.Tensor | None = None, q: Mx | None = None,
                     stream=None):
     """s = x + r (r None: x); sum = s, y = s / sqrt(mean(s^2) + eps) * gamma and q = y quantised, each where
-    given (at least one of y and q). sum or y may be x or r itself. Returns (sum, y, q)."""
+    given (at least one of y and q). sum or y may be x or r itself, and column slices of one buffer may be any
+    of the four. Returns (sum, y, q)."""
     ld = _rows(x, "x")
     n, n_in = x.shape
     if not isinstance(gamma, torch.Tensor) or gamma.dtype != torch.float32:

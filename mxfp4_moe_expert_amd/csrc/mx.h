@@ -102,16 +102,28 @@ inline bool mx_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0
 inline size_t type_size(int type) { return type == K3G_F32 ? 4 : 2; }
 inline bool type_ok(int type) { return type == K3G_F32 || type == K3G_BF16 || type == K3G_F16; }
 
-// A range of addresses a call touches. `n` rows, `stride` apart, of which the
-// last is `width` long: its end is exact, the gaps between rows count as used.
+// The addresses a call touches: one range, or (pitch not 0) rows of `width` bytes,
+// `pitch` apart, of which the last ends at hi. Two sets of rows of one pitch meet
+// where rows do; next to anything else the gaps between rows count as used.
 struct Span {
     uintptr_t lo, hi;
+    size_t pitch = 0, width = 0;
 };
 inline Span span(const void *p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
 inline Span rows_span(const void *p, int type, int64_t n, int64_t stride, int64_t width) {
-    return span(p, p && n > 0 ? type_size(type) * (size_t)((n - 1) * stride + width) : 0);
+    if (!p || n < 1) return span(p, 0);
+    Span s = span(p, type_size(type) * (size_t)((n - 1) * stride + width));
+    s.pitch = type_size(type) * (size_t)stride;
+    s.width = type_size(type) * (size_t)width;
+    return s;
 }
-inline bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+inline bool meet(const Span &a, const Span &b) {
+    if (a.lo >= b.hi || b.lo >= a.hi) return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    // a row of b begins d behind one of a's, and the next of a's pitch - d behind that
+    const size_t back = (a.lo - b.lo) % a.pitch, d = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : back ? a.pitch - back : 0;
+    return d < a.width || a.pitch - d < b.width;
+}
 
 inline size_t mx_code_bytes(const k3g_mx &m) { return (size_t)m.rows * m.in / (m.format == K3G_MXFP4 ? 2 : 1); }
 inline Span codes_span(const k3g_mx &m) { return span(m.codes, mx_code_bytes(m)); }
