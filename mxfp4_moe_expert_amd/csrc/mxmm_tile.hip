@@ -35,7 +35,8 @@ namespace k3g {
 
 // WR x WC wavefronts of FM x FN operand tiles (16 x 16) each, NB stages in LDS.
 // ODD: rows whose scale bytes start off 16-byte addresses or end inside four
-// stages; they come as five aligned dwords and are shifted into place.
+// stages; they come as five aligned dwords and are shifted into place (at a
+// tensor's ends, where a dword would reach outside it, byte by byte).
 template <int AF, int MODE_, int WR_, int WC_, int FM_, int FN_, int NB_, bool ODD_>
 struct Tile {
     static constexpr int MODE = MODE_, WR = WR_, WC = WC_, FM = FM_, FN = FN_, NB = NB_;
@@ -160,6 +161,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     uint32_t vw[C::DW], va[C::DA];
     const uint8_t *bw[C::DW], *ba;
     uint64_t s_addr;  // of the row whose scales this lane loads and prepares: a weight row, from lane MW on a token
+    int ends = 0;     // ODD: its first dword begins before the tensor (bit 0), its last ends behind it (bit 1)
     // the tile's entries of perm, fetched ahead (each wavefront its own tokens')
     int32_t *perm = (int32_t *)(lds + C::PERM_AT) + wave * kWave;
     auto fetch_perm = [&](const Item &o) {
@@ -188,6 +190,12 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
         for (int d = 0; d < C::DA; ++d) va[d] = (uint32_t)a_row(RA * d + lane / (64 / RA)) * a_pitch + 16 * ca;
         s_addr = is_w ? (uint64_t)(a.ws[w_tensor(iw)] + o.e * a.stride) + (uint64_t)(o.m0 + w_row(iw)) * a.G
                       : (uint64_t)a.a_scales + ((uint64_t)(gather ? 0 : o.p) + (uint64_t)a_row(ia_own)) * a.G;
+        if constexpr (C::ODD) {
+            const int row = is_w ? o.m0 + w_row(iw) : (gather ? 0 : o.p) + a_row(ia_own);
+            const int behind = (is_w ? a.rows : a.a_rows) - 1 - row;  // rows of the tensor
+            ends = (row < 3 && row * a.G < (int)(s_addr & 3) ? 1 : 0) |
+                   (behind < 3 && behind * a.G < 3 - (int)((s_addr + a.G - 1) & 3) ? 2 : 0);
+        }
     };
     auto issue = [&](int s, int buffer) {
         const uint32_t buf = lds0 + (uint32_t)buffer * C::STAGE;
@@ -203,18 +211,25 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             dma16(ba + C::AB * (int64_t)s, va[d] - backa, buf + C::BM * 64 + a0 * C::AB + 1024 * d);
     };
     const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
+    // ODD: the aligned dwords that hold the bytes of the stages 4u .. 4u + 3; past the row's last byte, the
+    // one that holds it. One with bytes outside the tensor is not read: its place takes some codes
+    // instead, and prepare_scales the row's bytes one by one.
+    auto scale_dword = [&](int u, int k) {
+        const uint64_t end = (s_addr + a.G - 1) & ~3ull, w = ((s_addr + 16 * (uint64_t)u) & ~3ull) + 4 * k;
+        return w < end ? w : end;
+    };
+    auto outside = [&](uint64_t w) {
+        return ((ends & 1) && w < s_addr) || ((ends & 2) && w + 4 > s_addr + a.G);
+    };
     auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
         if (!has_row) return;         // (lane 0 always has one)
-        const uint64_t at = s_addr + 16 * (uint64_t)u;
         if constexpr (!C::ODD) {
-            dma16_at((const void *)at, raw);
+            dma16_at((const void *)(s_addr + 16 * (uint64_t)u), raw);
         } else {
-            // the aligned dwords that hold the bytes; past the row's last byte, the one that holds it
-            const uint64_t end = (s_addr + a.G - 1) & ~3ull;
 #pragma unroll
             for (int k = 0; k < 5; ++k) {
-                const uint64_t w = (at & ~3ull) + 4 * k;
-                dma4_at((const void *)(w < end ? w : end), raw + 256 * k);
+                const uint64_t w = scale_dword(u, k);
+                dma4_at(outside(w) ? (const void *)a.a_codes : (const void *)w, raw + 256 * k);
             }
         }
     };
@@ -231,13 +246,22 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             const uint4 v = *(const uint4 *)(lds + C::RAW_AT + wave * C::RAW_W + 16 * lane);
             d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
         } else {
-            const uint32_t *v = (const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W) + lane;
-            uint32_t lo = v[0];
+            uint32_t v[5];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) v[k] = ((const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W))[64 * k + lane];
+            if (__ballot(ends != 0) != 0) {  // the tensors' first and last rows
+#pragma unroll
+                for (int k = 0; k < 5; ++k) {
+                    const uint64_t w = scale_dword(u, k);
+                    if (!outside(w)) continue;
+                    v[k] = 0;
+                    for (int b = 0; b < 4; ++b)
+                        if (w + b >= s_addr && w + b < s_addr + a.G) v[k] |= (uint32_t) * (const uint8_t *)(w + b) << (8 * b);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t hi = v[64 * (k + 1)];
-                d[k] = __builtin_amdgcn_alignbyte(hi, lo, (uint32_t)s_addr & 3u);
-                lo = hi;
+                d[k] = __builtin_amdgcn_alignbyte(v[k + 1], v[k], (uint32_t)s_addr & 3u);
                 const int left = a.G - 16 * u - 4 * k;  // groups from this stage on
                 if (left < 4) d[k] |= left > 0 ? ~0u << (8 * left) : ~0u;
             }
