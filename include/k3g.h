@@ -589,6 +589,14 @@ int k3g_probe_read_rate(const void *buf, size_t bytes, uint32_t *sink, void *str
  * 1 <= n_wg <= 65536; K3G_EINVAL otherwise. */
 int k3g_probe_handoff(int mode, int n_wg, float *buf, uint32_t *counter, void *stream);
 
+/* k3g_probe_mx_form: which kernel a microscaled product of these sizes runs on,
+ * without launching it: outputs << 16 | tokens of its tile, for kind 0
+ * k3g_mx_matmul (n_rows tokens, n_experts not read), 1 k3g_mx_grouped_matmul and
+ * 2 k3g_mx_grouped_glu (n_rows rows; outputs of the tile: of both weights
+ * together). rows: outputs. Tiles of up to 32 outputs are the streaming kernel's.
+ * K3G_EINVAL for a size that the call refuses. */
+int k3g_probe_mx_form(int a_format, int kind, int n_rows, int rows, int n_experts);
+
 #ifdef __cplusplus
 }
 #endif

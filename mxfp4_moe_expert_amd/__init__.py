@@ -140,6 +140,7 @@ def lib():
         L.k3g_probe_mfma_rate.argtypes = [i, i, P, P]
         L.k3g_probe_read_rate.argtypes = [P, sz, P, P]
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
+        L.k3g_probe_mx_form.argtypes = [i, i, i, i, i]
         _lib = L
     return _lib
 
@@ -684,6 +685,15 @@ def k3g_probe_handoff(mode: int, buf: torch.Tensor, counter: torch.Tensor, strea
     _dev(counter, torch.int32, "counter")
     _check("k3g_probe_handoff", lib().k3g_probe_handoff(mode, buf.numel() - 1, _ptr(buf), _ptr(counter),
                                                         _stream(stream)))
+
+
+def k3g_probe_mx_form(a_format: int, n_rows: int, rows: int, n_experts: int = 0, glu: bool = False) -> tuple[int, int]:
+    """(outputs, tokens) of the tile that a microscaled product of these sizes runs on: dense, or of a bank's experts.
+    Tiles of up to 32 outputs are the streaming kernel's."""
+    f = lib().k3g_probe_mx_form(a_format, 2 if glu else 1 if n_experts else 0, n_rows, rows, n_experts)
+    if f < 0:
+        _check("k3g_probe_mx_form", f)
+    return f >> 16, f & 0xFFFF
 
 
 def pack_bank(experts, n_experts: int, latent: int, inter: int, device="cuda", threads: int = 16):

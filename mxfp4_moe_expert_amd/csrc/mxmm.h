@@ -261,8 +261,11 @@ struct Items {
     }
 };
 
-// mxmm_tile.hip: the tiled kernels, and whether a dense product has enough of their smallest tiles to fill the chip
-int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st);
-bool tile_fills(const MmArgs &a);
+// The kernel that a product runs on: outputs << 16 | tokens of its weight rows' tile.
+constexpr int form(int rows, int tokens) { return rows << 16 | tokens; }
+
+// mxmm_tile.hip: the tile of a product (0: dense, with too few of the smallest to fill the chip), and its launch
+int tile_form(const MmArgs &a, int mode, int af);
+int launch_tile(const MmArgs &a, int mode, int af, int tile, hipStream_t st);
 
 }  // namespace k3g

@@ -175,13 +175,22 @@ int launch_stream(const MmArgs &a, hipStream_t st) {
 // Grouped products and dense ones with enough tiles of 128 x 32 run tiled (256
 // tokens at 7168 -> 3584: 20 us, here 19; 160 at 3584 -> 7168: 13, here 18; 96 at
 // 7168 -> 3584: 20, here 10).
+int product_form(const MmArgs &a, int mode, int af) {
+    if (const int tile = tile_form(a, mode, af)) return tile;
+    // up to 16 tokens 16 outputs a workgroup, while those are not more than a few rounds of the chip
+    if (a.T <= 16) return a.rows <= 16384 ? form(16, 16) : form(32, 16);
+    return a.T <= 32 ? form(32, 32) : form(32, 64);
+}
+
 template <int AF>
 int launch_product(const MmArgs &a, int mode, hipStream_t st) {
-    if (mode != DENSE || tile_fills(a)) return launch_tile(a, mode, AF, st);
-    // up to 16 tokens 16 outputs a workgroup, while those are not more than a few rounds of the chip
-    if (a.T <= 16) return a.rows <= 16384 ? launch_stream<AF, 1, 1>(a, st) : launch_stream<AF, 1, 2>(a, st);
-    if (a.T <= 32) return launch_stream<AF, 2, 2>(a, st);
-    return launch_stream<AF, 4, 2>(a, st);
+    switch (const int f = product_form(a, mode, AF)) {
+        case form(16, 16): return launch_stream<AF, 1, 1>(a, st);
+        case form(32, 16): return launch_stream<AF, 1, 2>(a, st);
+        case form(32, 32): return launch_stream<AF, 2, 2>(a, st);
+        case form(32, 64): return launch_stream<AF, 4, 2>(a, st);
+        default: return launch_tile(a, mode, AF, f, st);
+    }
 }
 
 int launch_any(const MmArgs &a, int mode, int af, hipStream_t st) {
@@ -333,6 +342,15 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
     m.T = n_rows, m.rows = bank->inter, m.in = bank->latent, m.G = bank->latent / kGroup;
     m.odd = odd_scales(m);
     return launch_any(m, GLU, a->format, (hipStream_t)stream);
+}
+
+int k3g_probe_mx_form(int a_format, int kind, int n_rows, int rows, int n_experts) {
+    if ((a_format != K3G_MXFP4 && a_format != K3G_MXFP8) || kind < DENSE || kind > GLU || n_rows < 1 || rows < 1 ||
+        n_rows > kMaxRows || rows > kMaxRows || (kind != DENSE && (n_experts < 1 || n_experts > kMaxExperts)))
+        return K3G_EINVAL;
+    MmArgs m = {};
+    m.T = n_rows, m.rows = rows, m.E = n_experts;
+    return product_form(m, kind, a_format);
 }
 
 }  // extern "C"

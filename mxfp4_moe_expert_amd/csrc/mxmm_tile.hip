@@ -520,47 +520,50 @@ struct Tiles {
     typedef Tile<AF, MODE, 2, 2, 4, 1, 4, ODD> T128x32;
 };
 
-template <class C>
-bool fills(const MmArgs &a) {
-    return ((int64_t)a.rows + C::OUT - 1) / C::OUT * (((int64_t)a.T + C::BN - 1) / C::BN) >= kFill;
+int tile_form(const MmArgs &a, int mode, int af) {
+    const bool fp4 = af == K3G_MXFP4;
+    if (mode != DENSE) {
+        if (a.T <= 8 * (int64_t)a.E) return form(128, 32);
+        return a.T <= 16 * (int64_t)a.E ? form(128, 64) : form(256, 128);
+    }
+    auto fills = [&](int bm, int bn) {
+        return ((int64_t)a.rows + bm - 1) / bm * (((int64_t)a.T + bn - 1) / bn) >= kFill;
+    };
+    if (fp4 && fills(256, 256)) return form(256, 256);
+    if (fills(256, 128)) return form(256, 128);
+    if (fp4 && fills(128, 128)) return form(128, 128);
+    if (fills(128, 64)) return form(128, 64);
+    return fills(128, 32) ? form(128, 32) : 0;
 }
 
 template <int AF, int MODE, bool ODD>
-int launch_mode(const MmArgs &a, hipStream_t st) {
+int launch_mode(const MmArgs &a, int tile, hipStream_t st) {
     typedef Tiles<AF, MODE, ODD> Ts;
-    if constexpr (MODE == DENSE) {
-        if constexpr (AF == K3G_MXFP4) {
-            if (fills<typename Ts::T256x256>(a)) return launch<AF, typename Ts::T256x256>(a, st);
-            if (fills<typename Ts::T256x128>(a)) return launch<AF, typename Ts::T256x128>(a, st);
-            if (fills<typename Ts::T128x128>(a)) return launch<AF, typename Ts::T128x128>(a, st);
-        } else {
-            if (fills<typename Ts::E256x128>(a)) return launch<AF, typename Ts::E256x128>(a, st);
-        }
-        if (fills<typename Ts::T128x64>(a)) return launch<AF, typename Ts::T128x64>(a, st);
-        return launch<AF, typename Ts::T128x32>(a, st);
-    } else {
-        if (a.T <= 8 * (int64_t)a.E) return launch<AF, typename Ts::T128x32>(a, st);
-        if (a.T <= 16 * (int64_t)a.E) return launch<AF, typename Ts::T128x64>(a, st);
-        if constexpr (AF == K3G_MXFP4)
-            return launch<AF, typename Ts::T256x128>(a, st);
-        else
-            return launch<AF, typename Ts::E256x128>(a, st);
+    if constexpr (AF == K3G_MXFP4 && MODE == DENSE) {
+        if (tile == form(256, 256)) return launch<AF, typename Ts::T256x256>(a, st);
+        if (tile == form(128, 128)) return launch<AF, typename Ts::T128x128>(a, st);
     }
+    if (tile == form(128, 64)) return launch<AF, typename Ts::T128x64>(a, st);
+    if (tile == form(128, 32)) return launch<AF, typename Ts::T128x32>(a, st);
+    if constexpr (AF == K3G_MXFP4)
+        return launch<AF, typename Ts::T256x128>(a, st);
+    else
+        return launch<AF, typename Ts::E256x128>(a, st);
 }
 
 template <int AF, bool ODD>
-int launch_af(const MmArgs &a, int mode, hipStream_t st) {
-    return mode == DENSE     ? launch_mode<AF, DENSE, ODD>(a, st)
-           : mode == GROUPED ? launch_mode<AF, GROUPED, ODD>(a, st)
-                             : launch_mode<AF, GLU, ODD>(a, st);
+int launch_af(const MmArgs &a, int mode, int tile, hipStream_t st) {
+    return mode == DENSE     ? launch_mode<AF, DENSE, ODD>(a, tile, st)
+           : mode == GROUPED ? launch_mode<AF, GROUPED, ODD>(a, tile, st)
+                             : launch_mode<AF, GLU, ODD>(a, tile, st);
 }
 
-bool tile_fills(const MmArgs &a) { return fills<Tiles<K3G_MXFP4, DENSE, false>::T128x32>(a); }
-
-int launch_tile(const MmArgs &a, int mode, int af, hipStream_t st) {
+int launch_tile(const MmArgs &a, int mode, int af, int tile, hipStream_t st) {
     if (a.odd)
-        return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, true>(a, mode, st) : launch_af<K3G_MXFP8, true>(a, mode, st);
-    return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, false>(a, mode, st) : launch_af<K3G_MXFP8, false>(a, mode, st);
+        return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, true>(a, mode, tile, st)
+                               : launch_af<K3G_MXFP8, true>(a, mode, tile, st);
+    return af == K3G_MXFP4 ? launch_af<K3G_MXFP4, false>(a, mode, tile, st)
+                           : launch_af<K3G_MXFP8, false>(a, mode, tile, st);
 }
 
 }  // namespace k3g

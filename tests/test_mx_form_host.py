@@ -1,0 +1,26 @@
+"""The kernel that a microscaled product runs on, as the host chooses it (CPU)."""
+import pytest
+
+EINVAL = -1
+
+
+@pytest.fixture(scope="module")
+def k3g():
+    import mxfp4_moe_expert_amd as k
+    return k
+
+
+def test_refusals(k3g):
+    f = k3g.lib().k3g_probe_mx_form
+    for bad in ((2, 0, 1, 1, 0), (-1, 0, 1, 1, 0), (0, 3, 1, 1, 1), (0, -1, 1, 1, 1), (0, 0, 0, 1, 0), (0, 0, 1, 0, 0),
+                (0, 1, 1, 1, 0), (0, 2, 1, 1, 2049), (0, 0, (1 << 30) + 1, 1, 0), (0, 0, 1, (1 << 30) + 1, 0)):
+        assert f(*bad) == EINVAL, bad
+    with pytest.raises(k3g.K3GError):
+        k3g.k3g_probe_mx_form(0, 0, 1)
+
+
+def test_forms(k3g):
+    form = k3g.k3g_probe_mx_form
+    assert form(k3g.MXFP8, 1, 3584) == (16, 16) and form(k3g.MXFP4, 61, 7168) == (32, 64)
+    assert form(k3g.MXFP4, 4096, 6144) == (256, 256) and form(k3g.MXFP8, 4096, 6144) == (256, 128)
+    assert form(k3g.MXFP8, 1024, 3584, 896) == (128, 32) and form(k3g.MXFP4, 65536, 3584, 896, glu=True) == (256, 128)
