@@ -120,7 +120,8 @@ __device__ inline void mul_column(const uint4 *w, const uint4 *t, const uint32_t
 }
 // Token tiles J0 + J... with the weights' tiles I0 .. I0+NI-1 (w, t: those tiles);
 // the wavefront has tokens in its first nf tiles only (uniform; a dense product's
-// tiles are nearly all full, and there the branches cost 5%).
+// tiles are all full but the last, itself more than half where it is the only
+// one, and there the branches cost 5%).
 template <int AF, class C, int PH, int I0, int NI, int J0, int... J>
 __device__ inline void mul_tiles(const uint4 *w, const uint4 (*t)[C::AB / 64], const uint32_t *sw, const uint32_t *st,
                                  float4_t (*acc)[C::FN], int nf, Seq<J...>) {
@@ -503,6 +504,12 @@ int launch(const MmArgs &a, hipStream_t st) {
 // 31 (448); 2048 tokens 256 x 128 40 (224), 128 x 128 43 (448). An e4m3 tile of
 // 128 x 128 has room for two stages on two workgroups only and loses to both its
 // neighbours (1024 tokens: 66 against 53 and 79).
+//
+// And no tile that the tokens fill to half or less: with outputs to fill the chip
+// whatever the tile, few tokens would multiply empty columns. 7168 -> 65536, MXFP4: 1 token 128 x 32 49-54, 256 x 256 77; 33 tokens
+// 128 x 64 54, 128 x 32 76, 256 x 256 79; 65 tokens 256 x 128 58, 128 x 64 79; 129
+// tokens 256 x 256 81, 256 x 128 91. MXFP8: 32 tokens 128 x 32 58, 128 x 64 69, 256 x
+// 128 98; 33 tokens 128 x 64 71, 128 x 32 89; 65 tokens 256 x 128 100, 128 x 64 121.
 constexpr int kFill = 160;
 
 // Grouped: by the rows an expert has on average over the whole bank (what the
@@ -527,7 +534,7 @@ int tile_form(const MmArgs &a, int mode, int af) {
         return a.T <= 16 * (int64_t)a.E ? form(128, 64) : form(256, 128);
     }
     auto fills = [&](int bm, int bn) {
-        return ((int64_t)a.rows + bm - 1) / bm * (((int64_t)a.T + bn - 1) / bn) >= kFill;
+        return (bn == 32 || a.T > bn / 2) && ((int64_t)a.rows + bm - 1) / bm * (((int64_t)a.T + bn - 1) / bn) >= kFill;
     };
     if (fp4 && fills(256, 256)) return form(256, 256);
     if (fills(256, 128)) return form(256, 128);

@@ -24,3 +24,14 @@ def test_forms(k3g):
     assert form(k3g.MXFP8, 1, 3584) == (16, 16) and form(k3g.MXFP4, 61, 7168) == (32, 64)
     assert form(k3g.MXFP4, 4096, 6144) == (256, 256) and form(k3g.MXFP8, 4096, 6144) == (256, 128)
     assert form(k3g.MXFP8, 1024, 3584, 896) == (128, 32) and form(k3g.MXFP4, 65536, 3584, 896, glu=True) == (256, 128)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_few_tokens_take_no_wide_tile(k3g, fmt):
+    """However many outputs: a tile of the tokens' width, or the streaming kernel."""
+    for rows in (3584, 16384, 20480, 40960, 65536, 131072, 1 << 20):
+        for T in (1, 2, 8, 16, 17, 31, 32, 33, 63, 64, 65, 100, 128):
+            outputs, tokens = k3g.k3g_probe_mx_form(fmt, T, rows)
+            assert tokens <= 32 or tokens < 2 * T, (rows, T, outputs, tokens)
+    assert k3g.k3g_probe_mx_form(fmt, 1, 131072) == (128, 32)
+    assert k3g.k3g_probe_mx_form(fmt, 129, 131072)[1] == (256 if fmt == 0 else 128)

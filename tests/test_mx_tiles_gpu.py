@@ -44,6 +44,8 @@ DENSE = [
     (0, 1010, 3584, (128, 128)),
     (0, 2500, 3570, (256, 128)), (1, 4090, 6136, (256, 128)),  # 280 and 768 items on 256 CUs
     (0, 4090, 6136, (256, 256)),  # 384
+    (0, 20, 110005, (128, 32)), (1, 20, 110005, (128, 32)),  # few tokens, 860 items
+    (0, 40, 70004, (128, 64)), (1, 40, 70004, (128, 64)),  # 547
 ]
 
 
