@@ -174,11 +174,18 @@ int launch_stream(const MmArgs &a, hipStream_t st) {
 
 // Grouped products and dense ones with enough tiles of 128 x 32 run tiled (256
 // tokens at 7168 -> 3584: 20 us, here 19; 160 at 3584 -> 7168: 13, here 18; 96 at
-// 7168 -> 3584: 20, here 10).
+// 7168 -> 3584: 20, here 10). Streamed, up to 16 tokens take 16 outputs a
+// workgroup while each of these has a CU of its own: in us, of 16 and 32 outputs, one
+// MXFP4 token 7168 -> 4096 7.5 and 9.3, 7168 -> 4608 11.7 and 9.1, MXFP8 8.4 and 9.8, 13.8
+// and 9.8; of 3584 inputs 6.1 and 6.5, 7.1 and 6.7, MXFP8 6.6 and 6.9, 7.7 and 7.2. Up to 32 tokens two
+// token tiles a workgroup, more four: 3584 -> 7168 (MXFP4, of one, two and four) 16
+// tokens 6.8, 6.9, -; 17 tokens 8.2, 7.3, -; 32 tokens 8.5, 7.5, 8.1; 33 tokens 11.3, 9.0,
+// 8.4; 64 tokens 13.0, 9.6, 9.2. (Where outputs are too few for the CUs, more workgroups
+// of fewer tokens are ahead: 7168 -> 3584, 17 tokens 8.9 and 10.3, 64 tokens of two and four
+// 10.2 and 13.4.)
 int product_form(const MmArgs &a, int mode, int af) {
     if (const int tile = tile_form(a, mode, af)) return tile;
-    // up to 16 tokens 16 outputs a workgroup, while those are not more than a few rounds of the chip
-    if (a.T <= 16) return a.rows <= 16384 ? form(16, 16) : form(32, 16);
+    if (a.T <= 16) return a.rows <= 16 * 256 ? form(16, 16) : form(32, 16);
     return a.T <= 32 ? form(32, 32) : form(32, 64);
 }
 

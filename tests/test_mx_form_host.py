@@ -35,3 +35,11 @@ def test_few_tokens_take_no_wide_tile(k3g, fmt):
             assert tokens <= 32 or tokens < 2 * T, (rows, T, outputs, tokens)
     assert k3g.k3g_probe_mx_form(fmt, 1, 131072) == (128, 32)
     assert k3g.k3g_probe_mx_form(fmt, 129, 131072)[1] == (256 if fmt == 0 else 128)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_one_token_takes_sixteen_outputs_while_each_has_a_cu(k3g, fmt):
+    for T in (1, 16):
+        assert k3g.k3g_probe_mx_form(fmt, T, 4096) == (16, 16)
+        for rows in (4097, 7168, 16384, 20000):
+            assert k3g.k3g_probe_mx_form(fmt, T, rows) == (32, 16)
