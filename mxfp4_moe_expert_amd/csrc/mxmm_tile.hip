@@ -513,10 +513,25 @@ int launch(const MmArgs &a, hipStream_t st) {
 constexpr int kFill = 160;
 
 // Grouped: by the rows an expert has on average over the whole bank (what the
-// host knows; a routing leaves some experts empty, so a group is larger). Up to
-// 8 rows the weights' bytes are all that counts: 32 tokens a tile, three
-// workgroups a CU. Measured at 896 experts (skewed: 290-350 with rows): 8192
-// rows 128 x 64 371 us, 256 x 128 382; 16384 rows 510 and 453.
+// host knows; a routing leaves some experts empty, so a group is larger). Measured at
+// 896 experts in us (w2, 3072 -> 3584, and the GLU), on a flat routing and on a skewed
+// one that meets 235-316 experts:
+//   rows          128 x 32     128 x 64     256 x 128
+//   1   MXFP4     617  1176    581  1172    616  1244
+//       MXFP8     680  1361    678  1381    804  1728
+//       skewed    268   524    264   517    272   557   (MXFP8 275 542, 274 550, 331 673)
+//   4.6 skewed    357   688    337   643    336   654   (MXFP8 383 763, 374 745, 418 857)
+//   8   MXFP4    1047  2033   1036  2012   1049  2072
+//       MXFP8    1113  2186   1118  2232   1260  2686
+//   9   skewed    472   903    412   794    402   818   (MXFP8 483 981, 434 889, 454 940)
+//   16  MXFP4    1124  2201   1107  2170   1110  2157
+//       MXFP8    1180  2372   1195  2394   1288  2739
+//       skewed    605  1140    496   947    445   921   (MXFP8 659 1379, 566 1206, 567 1187)
+//   24  MXFP4    1192  2353   1153  2279   1151  2238
+//       MXFP8    1288  2585   1250  2546   1315  2791
+//       skewed    815  1498    566  1089    498  1051   (MXFP8 906 1901, 730 1605, 682 1508)
+// So up to 2 rows 32 tokens (MXFP8's few rows; MXFP4 loses 6% there at most), up to 16
+// 64, and 128 beyond, where MXFP8 gains on a skewed routing what it loses on a flat one.
 template <int AF, int MODE, bool ODD>
 struct Tiles {
     typedef Tile<AF, MODE, 2, 4, 8, 4, 4, ODD> T256x256;  // e2m1
@@ -530,7 +545,7 @@ struct Tiles {
 int tile_form(const MmArgs &a, int mode, int af) {
     const bool fp4 = af == K3G_MXFP4;
     if (mode != DENSE) {
-        if (a.T <= 8 * (int64_t)a.E) return form(128, 32);
+        if (a.T <= 2 * (int64_t)a.E) return form(128, 32);
         return a.T <= 16 * (int64_t)a.E ? form(128, 64) : form(256, 128);
     }
     auto fills = [&](int bm, int bn) {

@@ -43,3 +43,11 @@ def test_one_token_takes_sixteen_outputs_while_each_has_a_cu(k3g, fmt):
         assert k3g.k3g_probe_mx_form(fmt, T, 4096) == (16, 16)
         for rows in (4097, 7168, 16384, 20000):
             assert k3g.k3g_probe_mx_form(fmt, T, rows) == (32, 16)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_grouped_borders(k3g, fmt, glu):
+    for E in (1, 8, 896):
+        for per, tile in ((1, (128, 32)), (2, (128, 32)), (3, (128, 64)), (16, (128, 64)), (17, (256, 128))):
+            assert k3g.k3g_probe_mx_form(fmt, E * per, 3584, E, glu) == tile

@@ -82,7 +82,7 @@ def test_dense(k3g, fmt, T, rows, tile, n):
 
 GROUPED = [
     # format, experts, rows an expert on average, tile: more items than run at once
-    (0, 200, 4, (128, 32)), (1, 200, 4, (128, 32)),
+    (0, 300, 2, (128, 32)), (1, 300, 2, (128, 32)),
     (0, 120, 12, (128, 64)), (1, 120, 12, (128, 64)),
     (0, 80, 40, (256, 128)), (1, 80, 40, (256, 128)),
 ]
