@@ -162,7 +162,11 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     uint32_t vw[C::DW], va[C::DA];
     const uint8_t *bw[C::DW], *ba;
     uint64_t s_addr;  // of the row whose scales this lane loads and prepares: a weight row, from lane MW on a token
-    int ends = 0;     // ODD: its first dword begins before the tensor (bit 0), its last ends behind it (bit 1)
+    // ODD: its first dword begins before the tensor (bit 0), its last ends behind it (bit 1); whether some
+    // lane's does (uniform); and then the two dwords, of the row's own bytes
+    int ends = 0;
+    bool edged = false;
+    uint32_t edge[2];
     // the tile's entries of perm, fetched ahead (each wavefront its own tokens')
     int32_t *perm = (int32_t *)(lds + C::PERM_AT) + wave * kWave;
     auto fetch_perm = [&](const Item &o) {
@@ -196,6 +200,19 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             const int behind = (is_w ? a.rows : a.a_rows) - 1 - row;  // rows of the tensor
             ends = (row < 3 && row * a.G < (int)(s_addr & 3) ? 1 : 0) |
                    (behind < 3 && behind * a.G < 3 - (int)((s_addr + a.G - 1) & 3) ? 2 : 0);
+            edged = __ballot(ends != 0) != 0;
+            if (edged) {  // (loaded here: prepare_scales comes a round of loads later)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    edge[k] = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint64_t last = s_addr + a.G - 1, at = ((k ? last : s_addr) & ~3ull) + b;
+                        const uint32_t byte = *(const uint8_t *)(at < s_addr ? s_addr : at > last ? last : at);
+                        edge[k] |= at < s_addr || at > last ? 0u : byte << (8 * b);
+                    }
+                }
+            }
         }
     };
     auto issue = [&](int s, int buffer) {
@@ -214,20 +231,22 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
     const uint32_t raw = lds0 + C::RAW_AT + wave * C::RAW_W;
     // ODD: the aligned dwords that hold the bytes of the stages 4u .. 4u + 3; past the row's last byte, the
     // one that holds it. One with bytes outside the tensor is not read: its place takes some codes
-    // instead, and prepare_scales the row's bytes one by one.
+    // instead, and prepare_scales what `edge` has.
     auto scale_dword = [&](int u, int k) {
         const uint64_t end = (s_addr + a.G - 1) & ~3ull, w = ((s_addr + 16 * (uint64_t)u) & ~3ull) + 4 * k;
         return w < end ? w : end;
     };
-    auto outside = [&](uint64_t w) {
-        return ((ends & 1) && w < s_addr) || ((ends & 2) && w + 4 > s_addr + a.G);
+    auto outside = [&](uint64_t w) {  // 1: before the tensor, 2: behind it, 0: neither
+        return (ends & 1) && w < s_addr ? 1 : (ends & 2) && w + 4 > s_addr + a.G ? 2 : 0;
     };
     auto issue_scales = [&](int u) {  // of the stages 4u .. 4u + 3
         if (!has_row) return;         // (lane 0 always has one)
         if constexpr (!C::ODD) {
             dma16_at((const void *)(s_addr + 16 * (uint64_t)u), raw);
-        } else {
+        } else if (!edged) {
 #pragma unroll
+            for (int k = 0; k < 5; ++k) dma4_at((const void *)scale_dword(u, k), raw + 256 * k);
+        } else {
             for (int k = 0; k < 5; ++k) {
                 const uint64_t w = scale_dword(u, k);
                 dma4_at(outside(w) ? (const void *)a.a_codes : (const void *)w, raw + 256 * k);
@@ -250,14 +269,11 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void mx_tile_kernel(MmArgs a)
             uint32_t v[5];
 #pragma unroll
             for (int k = 0; k < 5; ++k) v[k] = ((const uint32_t *)(lds + C::RAW_AT + wave * C::RAW_W))[64 * k + lane];
-            if (__ballot(ends != 0) != 0) {  // the tensors' first and last rows
+            if (edged) {
 #pragma unroll
                 for (int k = 0; k < 5; ++k) {
-                    const uint64_t w = scale_dword(u, k);
-                    if (!outside(w)) continue;
-                    v[k] = 0;
-                    for (int b = 0; b < 4; ++b)
-                        if (w + b >= s_addr && w + b < s_addr + a.G) v[k] |= (uint32_t) * (const uint8_t *)(w + b) << (8 * b);
+                    const int o = outside(scale_dword(u, k));
+                    v[k] = o == 1 ? edge[0] : o == 2 ? edge[1] : v[k];
                 }
             }
 #pragma unroll
