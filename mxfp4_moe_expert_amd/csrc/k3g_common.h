@@ -155,7 +155,7 @@ __device__ inline float exp_fast(float x) {
     constexpr float kL2E_LO = 1.92596299e-8f;  // log2(e) - kL2E
     const float t = x * kL2E;
     const float r = __builtin_fmaf(x, kL2E_LO, __builtin_fmaf(x, kL2E, -t));
-    const float part = __builtin_fminf(__builtin_fmaxf(r, -1.0f), 1.0f);  // (of a NaN r -1; a NaN x is one in 2^t)
+    const float part = __builtin_amdgcn_fmed3f(r, -1.0f, 1.0f);  // (of a NaN r -1; a NaN x is one in 2^t)
     return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(part, 0.693147182f, 1.0f);
 }
 
