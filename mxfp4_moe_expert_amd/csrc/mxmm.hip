@@ -241,7 +241,7 @@ int use_tensor(MmArgs *a, int slot, const k3g_expert_bank &b, int t, Span *cover
 }
 
 // What the two grouped calls check alike.
-int groups_ok(const k3g_mx *a, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows) {
+int groups_ok(const k3g_mx *a, const int32_t *offsets, const int32_t *perm, int n_rows) {
     if (!offsets) return K3G_EINVAL;
     if (n_rows > kMaxRows) return K3G_EUNSUPPORTED;
     if (!mx_aligned(offsets, 4) || (perm && !mx_aligned(perm, 4))) return K3G_EALIGN;
@@ -301,7 +301,7 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
     if (d.in != a->in || y_stride < d.rows) return K3G_EINVAL;
     if (n_rows == 0) return K3G_OK;
     if (!bank->base) return K3G_EINVAL;
-    K3G_TRY(groups_ok(a, offsets, perm, top_k, n_rows));
+    K3G_TRY(groups_ok(a, offsets, perm, n_rows));
     K3G_TRY(dense_ok(y, y_type, y_stride, d.rows));
     MmArgs m = {};
     Span w[2];
@@ -328,7 +328,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
         return K3G_EINVAL;
     if (n_rows == 0) return K3G_OK;
     if (!bank->base) return K3G_EINVAL;
-    K3G_TRY(groups_ok(a, offsets, perm, top_k, n_rows));
+    K3G_TRY(groups_ok(a, offsets, perm, n_rows));
     MmArgs m = {};
     Span w[4];
     K3G_TRY(use_tensor(&m, 0, *bank, K3G_W1, w));
