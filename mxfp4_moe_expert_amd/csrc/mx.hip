@@ -201,8 +201,8 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormArgs a) {
 }
 
 // Threads a row: with rows to fill the chip many times over, up to 512 (several
-// workgroups on a CU hide each other's waits: 8192 bf16 rows of 7168 in 81 us, 5.1 TB/s;
-// 84 with 896 threads a row, 88 with 256); with few rows, eight entries a thread.
+// workgroups on a CU hide each other's waits: 8192 bf16 rows of 7168 in 83-90 us, 4.6-5.0
+// TB/s; 3% more with 896 threads a row, 8% with 256); with few rows, eight entries a thread.
 template <int TYPE, int FMT>
 int launch_norm(NormArgs a, int n_rows, hipStream_t st) {
     const int chunks = a.in / 8, wide = n_rows >= 1024 ? 512 : 1024;

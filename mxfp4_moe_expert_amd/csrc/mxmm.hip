@@ -22,13 +22,15 @@ namespace k3g {
 // A dense product of so few tokens that tiles of 128 rows would leave most CUs
 // idle: a workgroup takes 16 NT tokens and 16 TILES outputs and splits the rows'
 // length, each wavefront four steps of 128 entries at a time: their weights and
-// scales (4 KB a tile) are all in flight before the first product. The wavefronts' sums
+// scales (4 KB a tile) are all in flight before the first product, the tokens' codes
+// two steps ahead of it. The wavefronts' sums
 // meet in LDS and are added in wavefront order. Four consecutive lanes load 64
 // contiguous bytes of a row (the L2 serves that several times faster than 16 rows
 // in consecutive lanes) and a permutation brings them into operand order.
-// One MXFP8 token at 7168 -> 3584: 7.9 us for 14 MB, 61 MXFP4 tokens at 3584 ->
-// 7168: 8.3 us for 16 MB. Latency bounds both (a launch, a round of loads, the
-// sum over the wavefronts, a store); the bytes alone would take a third.
+// One MXFP8 token at 7168 -> 3584: 7.8 us for 14 MB, 61 MXFP4 tokens at 3584 ->
+// 7168: 8.3 us for 16 MB. Latency bounds both (a launch, two to three rounds of
+// loads in a row, the sum over the wavefronts, a store); the bytes alone would
+// take a third.
 constexpr int kSteps = 4;       // steps a wavefront loads together
 constexpr int stream_waves(int nt) { return nt == 1 ? 16 : 8; }  // most wavefronts of a workgroup
 

@@ -22,13 +22,16 @@
 // so the matrix cores have work across the barrier, and NB - 1 stages are in
 // flight or about to be read.
 //
-// Measured, MXFP4: 4096 tokens at 7168 -> 6144 (256 x 256) 118-129 us, 2.8-3.1
-// PFLOP/s; 65536 grouped rows at 896 experts (256 x 128) 0.88 ms, 1.6 PFLOP/s, and
-// their gated up-products 1.9 ms, of which the way out (SiTU, quantising) is 17%.
-// All run at about 120 G requests of 64 bytes a second to the L2, which bounds
-// them; the matrix cores are 30% busy. 1024 grouped MXFP8 rows that meet 230
-// experts (128 x 32): 258-286 us, 4.8-5.3 TB/s of HBM, which bounds those; the 16
-// experts of one token 48 us, 3.9 TB/s (one item a workgroup: start and end show).
+// Measured, MXFP4: 4096 tokens at 7168 -> 6144 (256 x 256) 117-130 us, 2.8-3.1
+// PFLOP/s; 65536 grouped rows at 896 experts (256 x 128) 0.81-0.89 ms, 1.6-1.8 PFLOP/s,
+// and their gated up-products 1.8-1.9 ms, of which the way out (SiTU, quantising) is
+// 18%. MXFP8: 240-258 us, 1.4-1.5 ms and 3.0-3.25 ms, two matrix instructions an operand
+// pair. The matrix cores are 30% busy and the L2 serves 118-121 G requests a second
+// (64 bytes a row and stage, and 16 of scales), neither at its limit: loads alone take
+// 90 of the dense product's 120 us (158 G a second), products alone 85, and they overlap
+// in part only, all wavefronts in step at one barrier a stage. 1024 grouped MXFP8 rows
+// that meet 230 experts (128 x 32): 255-291 us, 4.7-5.3 TB/s of HBM, which bounds those;
+// the 16 experts of one token 48 us, 3.9 TB/s (one item a workgroup: start and end show).
 #include "mxmm.h"
 
 namespace k3g {
@@ -550,7 +553,7 @@ constexpr int kFill = 160;
 // 64, and 128 beyond, where MXFP8 gains on a skewed routing what it loses on a flat one.
 template <int AF, int MODE, bool ODD>
 struct Tiles {
-    typedef Tile<AF, MODE, 2, 4, 8, 4, 4, ODD> T256x256;  // e2m1
+    typedef Tile<AF, MODE, 2, 4, 8, 4, 4, ODD> T256x256;  // e2m1; all 256 registers, and 6 spilled (17 for ODD)
     typedef Tile<AF, MODE, 4, 2, 4, 4, 4, ODD> T256x128;  // e2m1
     typedef Tile<AF, MODE, 2, 4, 8, 2, 3, ODD> E256x128;  // e4m3: a token tile is cut once for eight weight tiles
     typedef Tile<AF, MODE, 2, 2, 4, 4, 3, ODD> T128x128;  // e2m1
