@@ -499,14 +499,14 @@ int k3g_mx_dequantize(void *y, int y_type, int64_t y_stride, const k3g_mx *q, vo
 
 /* The residual's addition and the RMS norm of each of n_rows rows of `in`
  * entries: s = x + r in fp32 (s = x where r is null), n = s / sqrt(mean(s^2) +
- * eps) * gamma, the mean in 64 bits from the unrounded s and n to 2^-46 of
- * itself. Written where the pointer is not null: sum = s and y = n, each rounded
- * once to `type`, and q = n quantised as k3g_mx_quantize does from the unrounded n (q->rows =
- * n_rows, q->in = in). At least one of y and q. x, r, sum and y are of `type`,
- * rows x_stride, r_stride, sum_stride, y_stride entries apart (each >= in);
- * gamma fp32 [in]; eps >= 0 (with eps = 0 a row of zeros is 0 / 0: NaN in y, byte 255
- * in q). sum or y may be x or r itself (same pointer and stride). in as
- * k3g_mx. */
+ * eps) * gamma, the mean in 64 bits from the unrounded s and n to 2^-46 of itself
+ * (or to 2^-149, fp32's smallest step). Written where the pointer is not null:
+ * sum = s and y = n, each rounded once to `type`, and q = n quantised as
+ * k3g_mx_quantize does from the unrounded n (q->rows = n_rows, q->in = in). At
+ * least one of y and q. x, r, sum and y are of `type`, rows x_stride, r_stride,
+ * sum_stride, y_stride entries apart (each >= in); gamma fp32 [in]; eps >= 0
+ * (with eps = 0 a row of zeros is 0 / 0: NaN in y, byte 255 in q). sum or y may be
+ * x or r itself (same pointer and stride). in as k3g_mx. */
 int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, const k3g_mx *q,
                     const void *x, int64_t x_stride, const void *r, int64_t r_stride, int type,
                     const float *gamma, float eps, int n_rows, int in, void *stream);
@@ -515,8 +515,7 @@ int k3g_add_rmsnorm(void *y, int64_t y_stride, void *sum, int64_t sum_stride, co
  * microscaled a [T][in] and an MXFP4 w [rows][in]: the block-scaled matrix
  * cores on both as they are stored, products exact, sums in fp32, rounded once
  * to y_type. y rows y_stride >= w->rows entries apart; at most 2^30 rows of a
- * and of w. A group with byte 255 in
- * a or in w adds nothing (e4m3 NaN codes, which the quantiser does not
+ * and of w. A group with byte 255 in a or in w adds nothing (e4m3 NaN codes, which the quantiser does not
  * write, propagate wherever a's byte is not 255). y must overlap no input. */
 int k3g_mx_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a, const k3g_mxfp4 *w, void *stream);
 
