@@ -291,7 +291,7 @@ def _own(s):
     if op == "sort":
         return k3g.k3g_moe_sort(ids(E + 1), ids(P), ids(T, K), s["idx"], s["ws"])
     if op == "gather":
-        y = k3g.k3g_moe_gather(s["s_out"], s["x"], s["perm"], K, wts=s["w"])
+        y = k3g.k3g_moe_gather(s["s_out"], s["x"], s["inv"], wts=s["w"])
         dx = new(T, c["n"], c["type"])
         if s["w"] is None:
             k3g.k3g_moe_gather_backward(dx, s["s"], s["inv"])
