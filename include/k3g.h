@@ -158,12 +158,14 @@ typedef enum {
     K3G_OP_EXPERT_GLU = 1,
     K3G_OP_MOE_ROUTE = 2,
     K3G_OP_MOE_LAYER = 3,
-    K3G_OP_LATENT_BLOCK = 4
+    K3G_OP_LATENT_BLOCK = 4,
+    K3G_OP_MOE_SORT = 5
 } k3g_op;
 
 /* Sizes that fix a workspace. Fields an op does not use are ignored:
  * EXPERT_GLU uses latent, inter, mode; MOE_ROUTE uses n_tokens, n_experts;
- * MOE_LAYER adds top_k, latent, inter, mode; LATENT_BLOCK uses all. */
+ * MOE_LAYER adds top_k, latent, inter, mode; LATENT_BLOCK uses all; MOE_SORT
+ * uses n_tokens, top_k, n_experts (its counts region: a histogram a chunk of pairs). */
 typedef struct {
     int32_t n_tokens, top_k, n_experts, latent, inter, hidden, sh_inter, mode;
 } k3g_shape;
@@ -542,6 +544,55 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
  * h are independent). h must overlap no input. */
 int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *bank, const int32_t *offsets,
                        const int32_t *perm, int top_k, int n_rows, void *stream);
+
+/* ---- routed pairs: sorted by expert, rows gathered and combined, and the gradients ---- */
+
+/* Pair q = t*top_k+k of a batch names expert idx[t][k]; an id outside [0,
+ * n_experts) (k3g_moe_route_topp's -1) is a dropped pair. Stable by (expert, q):
+ *   offsets int32 [n_experts+1]: pairs before each expert's; offsets[n_experts]
+ *           is the number of pairs that are kept;
+ *   perm    int32 [T*top_k]: sorted row -> pair, -1 from offsets[n_experts] on;
+ *   inv     int32 [T][top_k]: pair -> sorted row, -1 for a dropped pair.
+ * A token may name an expert more than once. These are the offsets and perm that
+ * the grouped products take. n_experts <= 2048, n_tokens * top_k <= 2^30
+ * (K3G_EUNSUPPORTED beyond). ws: k3g_workspace_bytes(K3G_OP_MOE_SORT, ...) bytes,
+ * 256-byte aligned. n_tokens = 0 writes offsets (all 0); the other pointers may
+ * then be null. */
+int k3g_moe_sort(int32_t *offsets, int32_t *perm, int32_t *inv, const int32_t *idx, int n_tokens, int top_k,
+                 int n_experts, void *ws, size_t ws_bytes, void *stream);
+
+/* Rows of tokens (x, y and their gradients; [T][in]) to and from sorted rows (ys
+ * and its gradient; [n_rows][in]), by the inv and, where not null, the weights
+ * wts fp32 [T][top_k] (null: all 1). Rows `stride` entries apart, each matrix of
+ * its own k3g_type (a gradient has its matrix's); sums and products in fp32,
+ * each result rounded once. An inv outside [0, n_rows) is a pair without a row:
+ * nothing is read, written or added for it, its weight is not read and its
+ * weight's gradient is 0. Precondition (not checked on the device; nothing out of
+ * range is touched without it): no sorted row is named twice. Sorted rows that
+ * inv does not name are left as they were.
+ *   gather:  ys[inv[t][k]] = wts[t][k] * x[t]
+ *   combine: y[t] = sum over k, ascending, of wts[t][k] * ys[inv[t][k]] (0 where t has no row)
+ * 1 <= top_k <= 64, in <= 65536, n_tokens * top_k and n_rows <= 2^30
+ * (K3G_EUNSUPPORTED beyond). n_tokens = 0: nothing is enqueued. */
+int k3g_moe_gather(void *ys, int ys_type, int64_t ys_stride, const void *x, int x_type, int64_t x_stride,
+                   const float *wts, const int32_t *inv, int n_tokens, int top_k, int n_rows, int in, void *stream);
+int k3g_moe_combine(void *y, int y_type, int64_t y_stride, const void *ys, int ys_type, int64_t ys_stride,
+                    const float *wts, const int32_t *inv, int n_tokens, int top_k, int n_rows, int in, void *stream);
+
+/* The gradients, from dys of a gather:
+ *   dx[t] = sum over k of wts[t][k] * dys[inv[t][k]],  dwts[t][k] = <x[t], dys[inv[t][k]]>
+ * and from dy of a combine:
+ *   dys[inv[t][k]] = wts[t][k] * dy[t],  dwts[t][k] = <dy[t], ys[inv[t][k]]>
+ * Either result may be null, not both; x and ys are read for dwts only (null
+ * without it; their type says dx's and dys's). dwts fp32 [T][top_k]. dys of a
+ * combine may be ys itself (same pointer and stride). Sums are in a fixed order:
+ * the same call gives the same bits. */
+int k3g_moe_gather_backward(void *dx, float *dwts, const void *dys, int dys_type, int64_t dys_stride, const void *x,
+                            int x_type, int64_t x_stride, int64_t dx_stride, const float *wts, const int32_t *inv,
+                            int n_tokens, int top_k, int n_rows, int in, void *stream);
+int k3g_moe_combine_backward(void *dys, float *dwts, const void *dy, int dy_type, int64_t dy_stride, const void *ys,
+                             int ys_type, int64_t ys_stride, int64_t dys_stride, const float *wts, const int32_t *inv,
+                             int n_tokens, int top_k, int n_rows, int in, void *stream);
 
 /* ---- stage hooks used by the bit-exact checks ----------------------------- */
 

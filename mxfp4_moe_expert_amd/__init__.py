@@ -10,7 +10,8 @@ The names match the C entry points: k3g_mxfp4_gemv, k3g_expert_glu,
 k3g_moe_route, k3g_moe_layer, k3g_latent_moe_block, k3g_quantize_i8_groups,
 k3g_mxfp4_idot_groupsums, and for microscaled activations k3g_mx_quantize,
 k3g_mx_dequantize, k3g_add_rmsnorm, k3g_mx_matmul, k3g_mx_grouped_matmul,
-k3g_mx_grouped_glu.
+k3g_mx_grouped_glu; for routed pairs k3g_moe_sort, k3g_moe_gather,
+k3g_moe_combine and their gradients.
 """
 
 from __future__ import annotations
@@ -34,6 +35,7 @@ OP_EXPERT_GLU = 1
 OP_MOE_ROUTE = 2
 OP_MOE_LAYER = 3
 OP_LATENT_BLOCK = 4
+OP_MOE_SORT = 5
 GROUP = 32
 MXFP4, MXFP8 = 0, 1  # microscaled row formats: e2m1 (two a byte) and e4m3 codes, a ue8m0 scale per 32 entries
 W1, W3, W2 = 0, 1, 2  # a bank's tensors as k3g_mx_grouped_matmul names them
@@ -137,6 +139,11 @@ def lib():
         L.k3g_mx_matmul.argtypes = [P, i, i64, P, P, P]
         L.k3g_mx_grouped_matmul.argtypes = [P, i, i64, P, P, i, P, P, i, i, P]
         L.k3g_mx_grouped_glu.argtypes = [P, P, P, P, P, i, i, P]
+        L.k3g_moe_sort.argtypes = [P, P, P, P, i, i, i, P, sz, P]
+        L.k3g_moe_gather.argtypes = [P, i, i64, P, i, i64, P, P, i, i, i, i, P]
+        L.k3g_moe_combine.argtypes = [P, i, i64, P, i, i64, P, P, i, i, i, i, P]
+        L.k3g_moe_gather_backward.argtypes = [P, P, P, i, i64, P, i, i64, i64, P, P, i, i, i, i, P]
+        L.k3g_moe_combine_backward.argtypes = [P, P, P, i, i64, P, i, i64, i64, P, P, i, i, i, i, P]
         L.k3g_probe_mfma_rate.argtypes = [i, i, P, P]
         L.k3g_probe_read_rate.argtypes = [P, sz, P, P]
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
@@ -658,6 +665,114 @@ def k3g_mx_grouped_glu(h: Mx, a: Mx, bank: ExpertBank, offsets: torch.Tensor, pe
         h._ref, a._ref, C.byref(bank), offsets.data_ptr(), None if perm is None else perm.data_ptr(), top_k, h.rows,
         st))
     return h
+
+
+# ---- routed pairs -------------------------------------------------------------
+
+def k3g_moe_sort(offsets: torch.Tensor, perm: torch.Tensor, inv: torch.Tensor, idx: torch.Tensor, ws: torch.Tensor,
+                 stream=None):
+    """The pairs of idx [T, K] sorted by expert, stably: offsets [n_experts + 1], perm [T * K] (sorted row -> pair
+    t * K + k, -1 behind the last) and inv [T, K] (pair -> sorted row, -1 for an id outside the experts). ws:
+    workspace(OP_MOE_SORT, shape(n_tokens, top_k, n_experts)). Returns (offsets, perm, inv)."""
+    for name, t in (("offsets", offsets), ("perm", perm), ("inv", inv), ("idx", idx)):
+        _dev(t, torch.int32, name)
+    _dev(ws, torch.uint8, "ws")
+    if idx.dim() != 2 or inv.shape != idx.shape or perm.numel() != idx.numel() or offsets.numel() < 2:
+        raise ValueError("shape mismatch")
+    T, K = idx.shape
+    st = _launch_stream(stream, *[t.get_device() for t in (offsets, perm, inv, idx, ws)])
+    _check("k3g_moe_sort", lib().k3g_moe_sort(offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), idx.data_ptr(), T, K,
+                                              offsets.numel() - 1, ws.data_ptr(), ws.numel(), st))
+    return offsets, perm, inv
+
+
+def _pairs(tok, rows, inv, wts, dwts, stream, *others):
+    """What the calls on pairs' rows check alike; returns (T, K, rows, columns, stream)."""
+    _dev(inv, torch.int32, "inv")
+    if inv.dim() != 2:
+        raise ValueError("inv must be [T, K]")
+    T, K = inv.shape
+    devices = [inv.get_device(), tok.get_device(), rows.get_device()]
+    for name, t in (("wts", wts), ("dwts", dwts)):
+        if t is not None:
+            _dev(t, torch.float32, name)
+            if t.shape != inv.shape:
+                raise ValueError(f"{name} must be [T, K]")
+            devices.append(t.get_device())
+    devices += [t.get_device() for t in others if t is not None]
+    return T, K, rows.shape[0], rows.shape[1], _launch_stream(stream, *devices)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def k3g_moe_gather(ys: torch.Tensor, x: torch.Tensor, inv: torch.Tensor, wts: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """ys[inv[t, k]] = wts[t, k] * x[t] (wts None: 1); rows that inv does not name are left as they were. ys and x:
+    float32, bfloat16 or float16 each, rows may lie apart."""
+    ld = _rows(ys, "ys")
+    xld = _rows(x, "x", -1, ys.shape[1])
+    T, K, R, n, st = _pairs(x, ys, inv, wts, None, stream)
+    if x.shape[0] != T:
+        raise ValueError("x must have a row a token")
+    _check("k3g_moe_gather", lib().k3g_moe_gather(ys.data_ptr(), _TYPES[ys.dtype], ld, x.data_ptr(), _TYPES[x.dtype], xld,
+                                                  _opt(wts), inv.data_ptr(), T, K, R, n, st))
+    return ys
+
+
+def k3g_moe_combine(y: torch.Tensor, ys: torch.Tensor, inv: torch.Tensor, wts: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """y[t] = sum_k wts[t, k] * ys[inv[t, k]] in fp32, k ascending (wts None: 1); a pair with inv -1 adds nothing."""
+    ld = _rows(ys, "ys")
+    yld = _rows(y, "y", -1, ys.shape[1])
+    T, K, R, n, st = _pairs(y, ys, inv, wts, None, stream)
+    if y.shape[0] != T:
+        raise ValueError("y must have a row a token")
+    _check("k3g_moe_combine", lib().k3g_moe_combine(y.data_ptr(), _TYPES[y.dtype], yld, ys.data_ptr(), _TYPES[ys.dtype], ld,
+                                                    _opt(wts), inv.data_ptr(), T, K, R, n, st))
+    return y
+
+
+def k3g_moe_gather_backward(dx: torch.Tensor | None, dys: torch.Tensor, inv: torch.Tensor,
+                            wts: torch.Tensor | None = None, x: torch.Tensor | None = None,
+                            dwts: torch.Tensor | None = None, stream=None):
+    """The gradients of k3g_moe_gather from dys, ys's: dx[t] = sum_k wts[t, k] * dys[inv[t, k]] and, with x,
+    dwts[t, k] = <x[t], dys[inv[t, k]]> (0 for inv -1). Either may be None. dx is of x's type. Returns (dx, dwts)."""
+    ld = _rows(dys, "dys")
+    tok = dx if dx is not None else x
+    if tok is None or (dx is None and dwts is None) or (dwts is not None and x is None):
+        raise ValueError("dx, or x and dwts")
+    dld = 0 if dx is None else _rows(dx, "dx", -1, dys.shape[1])
+    xld = 0 if x is None else _rows(x, "x", tok.shape[0], dys.shape[1], tok.dtype)
+    T, K, R, n, st = _pairs(tok, dys, inv, wts, dwts, stream, x)
+    if tok.shape[0] != T:
+        raise ValueError("dx and x must have a row a token")
+    _check("k3g_moe_gather_backward", lib().k3g_moe_gather_backward(
+        _opt(dx), _opt(dwts), dys.data_ptr(), _TYPES[dys.dtype], ld, _opt(x if dwts is not None else None),
+        _TYPES[tok.dtype], xld, dld, _opt(wts), inv.data_ptr(), T, K, R, n, st))
+    return dx, dwts
+
+
+def k3g_moe_combine_backward(dys: torch.Tensor | None, dy: torch.Tensor, inv: torch.Tensor,
+                             wts: torch.Tensor | None = None, ys: torch.Tensor | None = None,
+                             dwts: torch.Tensor | None = None, stream=None):
+    """The gradients of k3g_moe_combine from dy, y's: dys[inv[t, k]] = wts[t, k] * dy[t] (other rows are left as they
+    were) and, with ys, dwts[t, k] = <dy[t], ys[inv[t, k]]> (0 for inv -1). Either may be None; dys is of ys's type and
+    may be ys itself. Returns (dys, dwts)."""
+    ld = _rows(dy, "dy")
+    rows = dys if dys is not None else ys
+    if rows is None or (dys is None and dwts is None) or (dwts is not None and ys is None):
+        raise ValueError("dys, or ys and dwts")
+    sld = 0 if dys is None else _rows(dys, "dys", -1, dy.shape[1])
+    yld = 0 if ys is None else _rows(ys, "ys", rows.shape[0], dy.shape[1], rows.dtype)
+    T, K, R, n, st = _pairs(dy, rows, inv, wts, dwts, stream, ys)
+    if dy.shape[0] != T:
+        raise ValueError("dy must have a row a token")
+    _check("k3g_moe_combine_backward", lib().k3g_moe_combine_backward(
+        _opt(dys), _opt(dwts), dy.data_ptr(), _TYPES[dy.dtype], ld, _opt(ys if dwts is not None else None),
+        _TYPES[rows.dtype], yld, sld, _opt(wts), inv.data_ptr(), T, K, R, n, st))
+    return dys, dwts
 
 
 # ---- bank packing (data placement only) -------------------------------------

@@ -58,6 +58,7 @@ int launch_moe_down_f4m(float *ypair, const uint8_t *hp, const BankDev &bank, co
                         int max_slots, hipStream_t st);
 bool f4_shape_ok(int latent, int inter);
 bool f4_bank_ok(const BankDev &b);
+int sort_chunks(int64_t P);
 int launch_dense_glu(float *h, const uint16_t *w1, const uint16_t *w3, const float *x, int T, int K, int N,
                      hipStream_t st);
 int launch_rmsnorm(float *n, const float *a, const float *gamma, int T, int len, float eps, hipStream_t st);
@@ -215,6 +216,14 @@ int layout(k3g_ws_layout *o, int op, const k3g_shape &s) {
         case K3G_OP_MOE_ROUTE: {
             if (s.n_tokens < 0 || s.n_experts < 1 || s.n_experts > kMaxExperts) return K3G_EINVAL;
             o->logits = c.take(logits_bytes(s.n_tokens, s.n_experts));
+            break;
+        }
+        case K3G_OP_MOE_SORT: {
+            const int64_t P = (int64_t)s.n_tokens * s.top_k;
+            if (s.n_tokens < 0 || s.top_k < 1 || s.n_experts < 1 || s.n_experts > kMaxExperts || P > ((int64_t)1 << 30))
+                return K3G_EINVAL;
+            const int chunks = sort_chunks(P);
+            if (chunks > 1) o->counts = c.take(sizeof(int32_t) * chunks * (size_t)s.n_experts);
             break;
         }
         case K3G_OP_MOE_LAYER:
