@@ -545,6 +545,52 @@ int k3g_mx_grouped_matmul(void *y, int y_type, int64_t y_stride, const k3g_mx *a
 int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *bank, const int32_t *offsets,
                        const int32_t *perm, int top_k, int n_rows, void *stream);
 
+/* ---- int4 weights with a scale per group of columns ------------------------------ */
+
+/* n_experts matrices W_e [rows x in], one behind the other (1: a plain matrix):
+ *   packed [n_experts][rows][in/2]: codes n of 0 .. 15, two per byte, the LOW nibble
+ *          is the even column;
+ *   scales [n_experts][rows][in/group] of scale_type (a k3g_type);
+ *   zeros  uint8 [n_experts][rows][in/group], or null: all 8;
+ * an element is (n - zero) * scale of its group. group 32, 64 or 128; in a positive
+ * multiple of group, at most 65536; rows <= 2^30, n_experts <= 2048
+ * (K3G_EUNSUPPORTED beyond). packed 16-byte aligned, scales to their type. */
+typedef struct {
+    const uint8_t *packed;
+    const void *scales;
+    const uint8_t *zeros;
+    int32_t n_experts, rows, in, group, scale_type;
+} k3g_int4;
+
+/* y[t][r] = sum over groups of scale_rg * sum_{c in g} (n_rc - zero_rg) x_tc for x
+ * [T][in] of x_type (x_stride entries between rows) and a single matrix w: the codes
+ * go to the matrix cores as they are, no weight is rounded. fp32 x goes in as three
+ * bf16 parts whose sum it is. Products are exact, sums fp32 (off by a few 2^-24 of
+ * sum scale * (n + zero) * |x|), y rounded once to y_type. An infinity or NaN in x
+ * makes all of its token's outputs infinite or NaN. y rows y_stride entries apart;
+ * y must overlap no input. At most 2^30 tokens. */
+int k3g_int4_matmul(void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int n_tokens,
+                    const k3g_int4 *w, void *stream);
+
+/* The same product grouped by expert over ragged groups, which k3g_moe_sort
+ * writes: rows offsets[e] .. offsets[e+1]-1 of y are expert e's, y[p] = W_e
+ * x[src(p)], src(p) = p, or perm[p] / top_k where perm is given (int32 [n_rows]).
+ * x has x_rows rows, without perm at least n_rows; y has n_rows. Groups may be
+ * empty; rows below offsets[0] or from offsets[n_experts] on are left as they were.
+ * Preconditions (not checked on the device, but nothing out of range is read or
+ * written without them): offsets ascending within [0, n_rows], perm values of the
+ * groups' rows in [0, x_rows * top_k). */
+int k3g_int4_grouped_matmul(void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int x_rows,
+                            const k3g_int4 *w, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows,
+                            void *stream);
+
+/* The experts' gated up-products, grouped the same way: h[p] = SiTU(w1 x, w3 x) of
+ * p's expert in fp32, rounded once to h_type. w1 and w3 of one shape, group and
+ * scale_type. */
+int k3g_int4_grouped_glu(void *h, int h_type, int64_t h_stride, const void *x, int x_type, int64_t x_stride, int x_rows,
+                         const k3g_int4 *w1, const k3g_int4 *w3, const int32_t *offsets, const int32_t *perm, int top_k,
+                         int n_rows, void *stream);
+
 /* ---- routed pairs: sorted by expert, rows gathered and combined, and the gradients ---- */
 
 /* Pair q = t*top_k+k of a batch names expert idx[t][k]; an id outside [0,

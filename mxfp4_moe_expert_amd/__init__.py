@@ -11,7 +11,8 @@ k3g_moe_route, k3g_moe_layer, k3g_latent_moe_block, k3g_quantize_i8_groups,
 k3g_mxfp4_idot_groupsums, and for microscaled activations k3g_mx_quantize,
 k3g_mx_dequantize, k3g_add_rmsnorm, k3g_mx_matmul, k3g_mx_grouped_matmul,
 k3g_mx_grouped_glu; for routed pairs k3g_moe_sort, k3g_moe_gather,
-k3g_moe_combine and their gradients.
+k3g_moe_combine and their gradients; for int4 weights k3g_int4_matmul,
+k3g_int4_grouped_matmul, k3g_int4_grouped_glu.
 """
 
 from __future__ import annotations
@@ -59,6 +60,11 @@ class Expert(C.Structure):
 class MxStruct(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int32), ("in_", C.c_int32),
                 ("format", C.c_int32)]
+
+
+class Int4Struct(C.Structure):
+    _fields_ = [("packed", C.c_void_p), ("scales", C.c_void_p), ("zeros", C.c_void_p), ("n_experts", C.c_int32),
+                ("rows", C.c_int32), ("in_", C.c_int32), ("group", C.c_int32), ("scale_type", C.c_int32)]
 
 
 class ExpertBank(C.Structure):
@@ -144,6 +150,9 @@ def lib():
         L.k3g_moe_combine.argtypes = [P, i, i64, P, i, i64, P, P, i, i, i, i, P]
         L.k3g_moe_gather_backward.argtypes = [P, P, P, i, i64, P, i, i64, i64, P, P, i, i, i, i, P]
         L.k3g_moe_combine_backward.argtypes = [P, P, P, i, i64, P, i, i64, i64, P, P, i, i, i, i, P]
+        L.k3g_int4_matmul.argtypes = [P, i, i64, P, i, i64, i, P, P]
+        L.k3g_int4_grouped_matmul.argtypes = [P, i, i64, P, i, i64, i, P, P, P, i, i, P]
+        L.k3g_int4_grouped_glu.argtypes = [P, i, i64, P, i, i64, i, P, P, P, P, i, i, P]
         L.k3g_probe_mfma_rate.argtypes = [i, i, P, P]
         L.k3g_probe_read_rate.argtypes = [P, sz, P, P]
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
@@ -773,6 +782,110 @@ def k3g_moe_combine_backward(dys: torch.Tensor | None, dy: torch.Tensor, inv: to
         _opt(dys), _opt(dwts), dy.data_ptr(), _TYPES[dy.dtype], ld, _opt(ys if dwts is not None else None),
         _TYPES[rows.dtype], yld, sld, _opt(wts), inv.data_ptr(), T, K, R, n, st))
     return dys, dwts
+
+
+# ---- int4 weights ---------------------------------------------------------------
+
+class Int4:
+    """A matrix of int4 weights, or one for each expert (k3g_int4): packed uint8 [rows, in/2] or [E, rows, in/2] (low
+    nibble = even column), scales float32, bfloat16 or float16 [..., in/group], zeros uint8 of the scales' shape or None
+    (8). An element is (code - zero) * scale."""
+
+    __slots__ = ("packed", "scales", "zeros", "n_experts", "rows", "n_in", "group", "device", "struct", "_ref")
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None):
+        _dev(packed, torch.uint8, "packed")
+        if not isinstance(scales, torch.Tensor) or scales.dtype not in _TYPES:
+            raise TypeError("scales must be a float32, bfloat16 or float16 tensor")
+        _dev(scales, scales.dtype, "scales")
+        if packed.dim() not in (2, 3) or scales.dim() != packed.dim() or scales.shape[:-1] != packed.shape[:-1]:
+            raise ValueError("packed must be [rows, in/2] or [E, rows, in/2], scales [..., in/group]")
+        n_in, groups = 2 * packed.shape[-1], scales.shape[-1]
+        if groups < 1 or n_in % groups or n_in // groups not in (32, 64, 128):
+            raise ValueError("groups must be of 32, 64 or 128 columns")
+        if zeros is not None:
+            _dev(zeros, torch.uint8, "zeros")
+            if zeros.shape != scales.shape:
+                raise ValueError("zeros must have the scales' shape")
+        if any(t is not None and t.get_device() != packed.get_device() for t in (scales, zeros)):
+            raise ValueError("packed, scales and zeros must be on one device")
+        self.packed, self.scales, self.zeros = packed, scales, zeros  # the struct holds raw device pointers
+        self.n_experts = packed.shape[0] if packed.dim() == 3 else 1
+        self.rows, self.n_in, self.group, self.device = packed.shape[-2], n_in, n_in // groups, packed.get_device()
+        self.struct = Int4Struct(packed.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                 self.n_experts, self.rows, n_in, self.group, _TYPES[scales.dtype])
+        self._ref = C.byref(self.struct)
+
+
+def int4(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None) -> Int4:
+    """The int4 weights of these tensors."""
+    return Int4(packed, scales, zeros)
+
+
+def _int4_arg(w, name: str) -> Int4:
+    if not isinstance(w, Int4):
+        raise TypeError(f"{name} must be an Int4 (see int4)")
+    return w
+
+
+def k3g_int4_matmul(y: torch.Tensor, x: torch.Tensor, w: Int4, stream=None) -> torch.Tensor:
+    """y [T, rows] = x [T, in] w^T, each of float32, bfloat16 or float16; rows may lie apart."""
+    _int4_arg(w, "w")
+    if w.n_experts != 1:
+        raise ValueError("w must be a single matrix (see k3g_int4_grouped_matmul)")
+    xld = _rows(x, "x", -1, w.n_in)
+    ld = _rows(y, "y", x.shape[0], w.rows)
+    st = _launch_stream(stream, y.get_device(), x.get_device(), w.device)
+    _check("k3g_int4_matmul", lib().k3g_int4_matmul(y.data_ptr(), _TYPES[y.dtype], ld, x.data_ptr(), _TYPES[x.dtype], xld,
+                                                    x.shape[0], w._ref, st))
+    return y
+
+
+def _int4_groups(y, x, w: Int4, offsets, perm, top_k: int, stream):
+    """What the grouped calls check alike; returns (y's row stride, x's, the stream)."""
+    xld = _rows(x, "x", -1, w.n_in)
+    ld = _rows(y, "the output", -1, w.rows)
+    _dev(offsets, torch.int32, "offsets")
+    if offsets.numel() != w.n_experts + 1:
+        raise ValueError("offsets must have n_experts + 1 entries")
+    devices = [y.get_device(), x.get_device(), w.device, offsets.get_device()]
+    if perm is not None:
+        _dev(perm, torch.int32, "perm")
+        if perm.numel() != y.shape[0]:
+            raise ValueError("perm must have an entry a row")
+        devices.append(perm.get_device())
+    elif x.shape[0] < y.shape[0]:
+        raise ValueError("without perm, x must have a row for each row of the output")
+    if top_k < 1:
+        raise ValueError("top_k must be positive")
+    return ld, xld, _launch_stream(stream, *devices)
+
+
+def k3g_int4_grouped_matmul(y: torch.Tensor, x: torch.Tensor, w: Int4, offsets: torch.Tensor,
+                            perm: torch.Tensor | None = None, top_k: int = 1, stream=None) -> torch.Tensor:
+    """y[p] = W_e x[p] (or x[perm[p] // top_k]) for the rows p of each expert e's group, offsets[e] .. offsets[e + 1] - 1
+    (k3g_moe_sort's). Rows outside the groups are left as they were."""
+    _int4_arg(w, "w")
+    ld, xld, st = _int4_groups(y, x, w, offsets, perm, top_k, stream)
+    _check("k3g_int4_grouped_matmul", lib().k3g_int4_grouped_matmul(
+        y.data_ptr(), _TYPES[y.dtype], ld, x.data_ptr(), _TYPES[x.dtype], xld, x.shape[0], w._ref, offsets.data_ptr(),
+        _opt(perm), top_k, y.shape[0], st))
+    return y
+
+
+def k3g_int4_grouped_glu(h: torch.Tensor, x: torch.Tensor, w1: Int4, w3: Int4, offsets: torch.Tensor,
+                         perm: torch.Tensor | None = None, top_k: int = 1, stream=None) -> torch.Tensor:
+    """h[p] = SiTU(w1 x, w3 x) of each row's expert; rows and groups as k3g_int4_grouped_matmul."""
+    _int4_arg(w1, "w1")
+    _int4_arg(w3, "w3")
+    if (w1.n_experts, w1.rows, w1.n_in, w1.group, w1.device, w1.scales.dtype) != (
+            w3.n_experts, w3.rows, w3.n_in, w3.group, w3.device, w3.scales.dtype):
+        raise ValueError("w1 and w3 must be of one shape, group and scale type, on one device")
+    ld, xld, st = _int4_groups(h, x, w1, offsets, perm, top_k, stream)
+    _check("k3g_int4_grouped_glu", lib().k3g_int4_grouped_glu(
+        h.data_ptr(), _TYPES[h.dtype], ld, x.data_ptr(), _TYPES[x.dtype], xld, x.shape[0], w1._ref, w3._ref,
+        offsets.data_ptr(), _opt(perm), top_k, h.shape[0], st))
+    return h
 
 
 # ---- bank packing (data placement only) -------------------------------------

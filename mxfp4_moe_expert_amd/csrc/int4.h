@@ -1,0 +1,146 @@
+// int4.h -- what the int4 product kernels share (int4.hip, int4_stream.h):
+// operands, codes on their way to the matrix cores, activations as operands.
+//
+// A weight is (n - z) s, n a code of 0 .. 15, s and z of its row's group of 32,
+// 64 or 128 columns. The matrix cores multiply the codes themselves, which are
+// exact in bf16 and fp16, and s is applied to the group's sum in fp32, so no
+// weight is ever rounded:
+//   y[t][r] = sum_g s_rg (sum_{c in g} n_rc x_tc - z_rg sum_{c in g} x_tc).
+// The sum of x is a product with ones; -z times it is what the product with the
+// codes starts from, so the two large numbers cancel inside the accumulation and
+// not in two rounded sums.
+#pragma once
+
+#include "mxmm.h"
+
+namespace k3g {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// One product, or the products of every expert of a stack of matrices.
+struct I4Args {
+    const uint8_t *w[2];     // packed codes (GLU: w1, w3)
+    const void *s[2];        // scales
+    const uint8_t *z[2];     // zeros, or null: 8
+    const void *x;
+    const int32_t *offsets, *perm;  // grouped: ragged groups, and the source rows (null: straight)
+    void *y;
+    int64_t xs, ys;          // entries between rows
+    int T;                   // rows of y (grouped: of all experts)
+    int x_rows;
+    int rows, in, G;         // outputs; entries and groups of a row
+    int E, top_k;
+    int s_type, y_type;
+};
+
+// Eight codes (a dword, the low nibble first) as bf16 or fp16, in order. A code
+// zero-extended to a byte is n 2^-9 read as e4m3 (up to 7 subnormal, 8 to 15
+// the lowest binade: one step throughout), so gfx950's scaled convert makes two of
+// them at a time: 9 instructions, against 16 by single converts from int4.
+template <int XT>
+__device__ inline uint4 codes8(uint32_t d) {
+    const uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;
+    const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+    if constexpr (XT == K3G_F16)
+        return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, true)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, true)));
+    else
+        return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true)));
+}
+
+// Eight entries of a token as operand A. fp32 goes in as three bf16 parts whose
+// sum it is: each the leading 8 bits of what the ones before leave.
+template <int XT>
+struct Act4;
+template <>
+struct Act4<K3G_BF16> {
+    uint4 v;
+    __device__ inline void load(const void *p) { __builtin_memcpy(&v, p, 16); }
+    __device__ inline float4_t mul(const uint4 &w, float4_t c) const {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, w), c, 0,
+                                                       0, 0);
+    }
+    static __device__ inline uint4 ones() { return make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u); }
+};
+template <>
+struct Act4<K3G_F16> {
+    uint4 v;
+    __device__ inline void load(const void *p) { __builtin_memcpy(&v, p, 16); }
+    __device__ inline float4_t mul(const uint4 &w, float4_t c) const {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, w), c, 0, 0,
+                                                      0);
+    }
+    static __device__ inline uint4 ones() { return make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u); }
+};
+template <>
+struct Act4<K3G_F32> {
+    uint4 part[3];
+    __device__ inline void load(const void *p) {
+        float f[8];
+        __builtin_memcpy(f, p, 32);
+        uint32_t d[3][4];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = __builtin_bit_cast(uint32_t, f[2 * i]), b = __builtin_bit_cast(uint32_t, f[2 * i + 1]);
+                d[k][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+                f[2 * i] -= __builtin_bit_cast(float, a & 0xFFFF0000u);
+                f[2 * i + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
+            }
+            part[k] = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+        }
+    }
+    __device__ inline float4_t mul(const uint4 &w, float4_t c) const {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, part[k]),
+                                                        __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
+        return c;
+    }
+    static __device__ inline uint4 ones() { return Act4<K3G_BF16>::ones(); }
+};
+
+// An entry of a scale tensor.
+__device__ inline float scale_at(const void *s, int type, int64_t i) {
+    return type == K3G_F32 ? ((const float *)s)[i] : type == K3G_BF16 ? (float)((const __bf16 *)s)[i] : (float)((const _Float16 *)s)[i];
+}
+// N consecutive ones, as fp32.
+template <int N>
+__device__ inline void scales_at(float *v, const void *s, int type, int64_t i) {
+    if (type == K3G_F32)
+        load_n<K3G_F32, N>(v, (const float *)s + i);
+    else if (type == K3G_BF16)
+        load_n<K3G_BF16, N>(v, (const __bf16 *)s + i);
+    else
+        load_n<K3G_F16, N>(v, (const _Float16 *)s + i);
+}
+
+__device__ inline void store_out(void *y, int type, int64_t i, float v) {
+    if (type == K3G_F32)
+        ((float *)y)[i] = v;
+    else if (type == K3G_BF16)
+        ((__bf16 *)y)[i] = (__bf16)v;
+    else
+        ((_Float16 *)y)[i] = (_Float16)v;
+}
+
+// The source row of row p of y.
+__device__ inline int source(const I4Args &a, int p) {
+    if (!a.perm) return p;
+    const int q = a.perm[p];
+    return min((int)((unsigned)max(q, 0) / (unsigned)a.top_k), a.x_rows - 1);
+}
+
+// int4_{f32,bf16,f16}.hip: a product's launch for activations of one type
+int launch_int4_f32(const I4Args &a, int mode, int group, hipStream_t st);
+int launch_int4_bf16(const I4Args &a, int mode, int group, hipStream_t st);
+int launch_int4_f16(const I4Args &a, int mode, int group, hipStream_t st);
+
+}  // namespace k3g

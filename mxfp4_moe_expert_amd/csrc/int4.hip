@@ -1,0 +1,111 @@
+// int4.hip -- products with int4 weights: the calls, their checks, and which
+// kernels they run on.
+#include "int4.h"
+
+using namespace k3g;
+
+namespace {
+
+constexpr int kMaxExperts = 2048;
+constexpr int kMaxRows = 1 << 30;  // tiles are counted in 32 bits
+
+// The matrices as the kernels' operand `slot`, and the addresses they cover.
+int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
+    if (!w || w->n_experts < 1 || w->rows < 1 || w->in < 1 || (w->group != 32 && w->group != 64 && w->group != 128) ||
+        w->in % w->group || !type_ok(w->scale_type))
+        return K3G_EINVAL;
+    if (w->n_experts > kMaxExperts || w->rows > kMaxRows || w->in > kMxMaxIn) return K3G_EUNSUPPORTED;
+    if (!w->packed || !w->scales) return K3G_EINVAL;
+    if (!mx_aligned(w->packed, 16) || !mx_aligned(w->scales, type_size(w->scale_type))) return K3G_EALIGN;
+    const size_t rows = (size_t)w->n_experts * w->rows, groups = rows * (w->in / w->group);
+    covers[0] = span(w->packed, rows * (w->in / 2));
+    covers[1] = span(w->scales, groups * type_size(w->scale_type));
+    covers[2] = span(w->zeros, w->zeros ? groups : 0);
+    a->w[slot] = w->packed, a->s[slot] = w->scales, a->z[slot] = w->zeros;
+    a->rows = w->rows, a->in = w->in, a->G = w->in / w->group, a->E = w->n_experts, a->s_type = w->scale_type;
+    return K3G_OK;
+}
+
+int launch(const I4Args &a, int mode, int x_type, int group, void *stream) {
+    hipStream_t st = (hipStream_t)stream;
+    return x_type == K3G_F32    ? launch_int4_f32(a, mode, group, st)
+           : x_type == K3G_BF16 ? launch_int4_bf16(a, mode, group, st)
+                                : launch_int4_f16(a, mode, group, st);
+}
+
+// The grouped calls' checks of everything but the weights; n_w spans of those in `use`.
+int groups(I4Args *a, void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int x_rows,
+           const int32_t *offsets, const int32_t *perm, int top_k, int n_rows, const Span *use, int n_w) {
+    if (!offsets || x_rows < 1 || (!perm && x_rows < n_rows)) return K3G_EINVAL;
+    if (!mx_aligned(offsets, 4) || !mx_aligned(perm, 4)) return K3G_EALIGN;
+    K3G_TRY(dense_ok(y, y_type, y_stride, a->rows));
+    K3G_TRY(dense_ok(x, x_type, x_stride, a->in));
+    const Span out = rows_span(y, y_type, n_rows, y_stride, a->rows);
+    for (int i = 0; i < n_w; ++i)
+        if (meet(out, use[i])) return K3G_EINVAL;
+    if (meet(out, rows_span(x, x_type, x_rows, x_stride, a->in)) || meet(out, span(offsets, 4 * ((size_t)a->E + 1))) ||
+        (perm && meet(out, span(perm, 4 * (size_t)n_rows))))
+        return K3G_EINVAL;
+    K3G_TRY(device_ok());
+    a->x = x, a->xs = x_stride, a->x_rows = x_rows, a->offsets = offsets, a->perm = perm, a->top_k = top_k;
+    a->y = y, a->ys = y_stride, a->y_type = y_type, a->T = n_rows;
+    return K3G_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int k3g_int4_matmul(void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int n_tokens,
+                    const k3g_int4 *w, void *stream) {
+    I4Args a = {};
+    Span use[3];
+    K3G_TRY(use_int4(&a, 0, w, use));
+    if (w->n_experts != 1 || n_tokens < 0 || !type_ok(y_type) || !type_ok(x_type) || y_stride < w->rows || x_stride < w->in)
+        return K3G_EINVAL;
+    if (n_tokens > kMaxRows) return K3G_EUNSUPPORTED;
+    if (n_tokens == 0) return K3G_OK;
+    K3G_TRY(dense_ok(y, y_type, y_stride, w->rows));
+    K3G_TRY(dense_ok(x, x_type, x_stride, w->in));
+    const Span out = rows_span(y, y_type, n_tokens, y_stride, w->rows);
+    for (const Span &s : use)
+        if (meet(out, s)) return K3G_EINVAL;
+    if (meet(out, rows_span(x, x_type, n_tokens, x_stride, w->in))) return K3G_EINVAL;
+    K3G_TRY(device_ok());
+    a.x = x, a.xs = x_stride, a.x_rows = n_tokens, a.y = y, a.ys = y_stride, a.y_type = y_type, a.T = n_tokens;
+    return launch(a, DENSE, x_type, w->group, stream);
+}
+
+int k3g_int4_grouped_matmul(void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int x_rows,
+                            const k3g_int4 *w, const int32_t *offsets, const int32_t *perm, int top_k, int n_rows,
+                            void *stream) {
+    I4Args a = {};
+    Span use[3];
+    K3G_TRY(use_int4(&a, 0, w, use));
+    if (n_rows < 0 || x_rows < 0 || top_k < 1 || !type_ok(y_type) || !type_ok(x_type) || y_stride < w->rows ||
+        x_stride < w->in)
+        return K3G_EINVAL;
+    if (n_rows > kMaxRows || x_rows > kMaxRows) return K3G_EUNSUPPORTED;
+    if (n_rows == 0) return K3G_OK;
+    K3G_TRY(groups(&a, y, y_type, y_stride, x, x_type, x_stride, x_rows, offsets, perm, top_k, n_rows, use, 3));
+    return launch(a, GROUPED, x_type, w->group, stream);
+}
+
+int k3g_int4_grouped_glu(void *h, int h_type, int64_t h_stride, const void *x, int x_type, int64_t x_stride, int x_rows,
+                         const k3g_int4 *w1, const k3g_int4 *w3, const int32_t *offsets, const int32_t *perm, int top_k,
+                         int n_rows, void *stream) {
+    I4Args a = {};
+    Span use[6];
+    K3G_TRY(use_int4(&a, 0, w1, use));
+    K3G_TRY(use_int4(&a, 1, w3, use + 3));
+    if (w1->n_experts != w3->n_experts || w1->rows != w3->rows || w1->in != w3->in || w1->group != w3->group ||
+        w1->scale_type != w3->scale_type || n_rows < 0 || x_rows < 0 || top_k < 1 || !type_ok(h_type) ||
+        !type_ok(x_type) || h_stride < w1->rows || x_stride < w1->in)
+        return K3G_EINVAL;
+    if (n_rows > kMaxRows || x_rows > kMaxRows) return K3G_EUNSUPPORTED;
+    if (n_rows == 0) return K3G_OK;
+    K3G_TRY(groups(&a, h, h_type, h_stride, x, x_type, x_stride, x_rows, offsets, perm, top_k, n_rows, use, 6));
+    return launch(a, GLU, x_type, w1->group, stream);
+}
+
+}  // extern "C"

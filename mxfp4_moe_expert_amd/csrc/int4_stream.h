@@ -1,0 +1,199 @@
+// int4_stream.h -- int4 products whose weights are streamed once: a workgroup
+// takes 16 NT rows of activations and 16 RT outputs (of one expert) and splits
+// the row's length over its wavefronts, 512 columns at a time, whose codes and
+// scales are all in flight before the first product. The wavefronts' sums meet in
+// LDS and are added in wavefront order.
+//
+// Operand A is the activations (16 tokens), operand B the codes (16 outputs):
+// lane l = r + 16 q holds columns 8q .. 8q+7 of token or output r of a block of 32
+// columns, and of the result output r of tokens 4q .. 4q+3, so that a group's scale
+// and zero are one number a lane. Four consecutive lanes load 64 contiguous bytes
+// of a row; a permutation over the wavefront and a transposition of the four
+// 16-lane rows bring the dword of (output r, columns 8q ..) of each of the four
+// blocks into place.
+#pragma once
+
+#include "int4.h"
+
+namespace k3g {
+
+constexpr int kI4Steps = 4;  // steps of 128 columns that a wavefront loads together
+constexpr int kI4Waves = 8;
+
+// v[c] of lane row q <-> v[q] of lane row c (a lane row: 16 lanes).
+__device__ inline void transpose4(uint32_t *v) {
+    auto s = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    auto t = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    auto a = __builtin_amdgcn_permlane16_swap(s[0], t[0], false, false);
+    auto b = __builtin_amdgcn_permlane16_swap(s[1], t[1], false, false);
+    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+}
+
+template <int XT, int GROUP, int MODE, int RT, int NT>
+__global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a) {
+    constexpr int NW = MODE == GLU ? 2 : 1, TILES = RT * NW, BLOCKS = GROUP / 32;
+    constexpr int NG = 128 * kI4Steps / GROUP;  // groups of a turn
+    constexpr int X = XT == K3G_F32 ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int waves = blockDim.x / kWave;
+    float4_t *part = (float4_t *)lds;  // [wave][tile][token tile][lane]
+    int32_t *table = (int32_t *)(part + (size_t)waves * TILES * NT * kWave);
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r = lane & 15, q = lane >> 4;   // as the operands have them
+    const int lr = lane >> 2, lq = lane & 3;  // as the codes are loaded
+    const int psrc = 4 * (4 * r + q);
+    const int units = a.in / 32, pitch = a.in / 2;
+    Items<MODE, 16 * NT, 16 * RT, I4Args> items(a, table, blockDim.x);
+    Item it;
+    while (items.next(it)) {
+        const uint8_t *wc[TILES], *zc[TILES];
+        int64_t sc[TILES];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int k = t / RT, m = it.m0 + 16 * (t % RT);
+            const int64_t row = (int64_t)it.e * a.rows;
+            wc[t] = a.w[k] + (row + min(m + lr, a.rows - 1)) * pitch;
+            sc[t] = (row + min(m + r, a.rows - 1)) * a.G;
+            zc[t] = a.z[k] + sc[t];
+        }
+        const uint8_t *xc[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            xc[j] = (const uint8_t *)a.x + X * ((int64_t)source(a, it.p + min(16 * j + r, it.n_tok - 1)) * a.xs + 8 * q);
+        float4_t acc[TILES][NT];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+        for (int u0 = 4 * kI4Steps * wave; u0 < units; u0 += 4 * kI4Steps * waves) {
+            uint4 w[kI4Steps][TILES];
+            float s[TILES][NG];
+            uint8_t z[TILES][NG];
+#pragma unroll
+            for (int i = 0; i < kI4Steps; ++i)
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) w[i][t] = load16(wc[t] + 16 * (int64_t)min(u0 + 4 * i + lq, units - 1));
+            const int g0 = u0 / BLOCKS;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                const void *sp = a.s[t / RT];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) z[t][g] = 8;
+                if (g0 + NG <= a.G) {
+                    scales_at<NG>(s[t], sp, a.s_type, sc[t] + g0);
+                    if (a.z[t / RT]) __builtin_memcpy(z[t], zc[t] + g0, NG);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const int at = min(g0 + g, a.G - 1);
+                        s[t][g] = scale_at(sp, a.s_type, sc[t] + at);
+                        if (a.z[t / RT]) z[t][g] = zc[t][at];
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kI4Steps; ++i) {
+                if (u0 + 4 * i >= units) break;
+                Act4<XT> x[NT][4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) x[j][b].load(xc[j] + X * 32 * (int64_t)min(u0 + 4 * i + b, units - 1));
+                uint32_t d[TILES][4];
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    const uint4 v = to_operand(w[i][t], psrc);
+                    d[t][0] = v.x, d[t][1] = v.y, d[t][2] = v.z, d[t][3] = v.w;
+                    transpose4(d[t]);
+                }
+#pragma unroll
+                for (int b = 0; b < 4; b += BLOCKS) {
+                    if (u0 + 4 * i + b >= units) break;
+                    const int g = (4 * i + b) / BLOCKS;
+                    float4_t sum[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        sum[j] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < BLOCKS; ++k) sum[j] = x[j][b + k].mul(Act4<XT>::ones(), sum[j]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) {
+                        uint4 codes[BLOCKS];
+#pragma unroll
+                        for (int k = 0; k < BLOCKS; ++k) codes[k] = codes8<XT>(d[t][b + k]);
+                        const float zero = -(float)z[t][g];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            float4_t p = zero * sum[j];
+#pragma unroll
+                            for (int k = 0; k < BLOCKS; ++k) p = x[j][b + k].mul(codes[k], p);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) acc[t][j][k] = __builtin_fmaf(s[t][g], p[k], acc[t][j][k]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) part[((wave * TILES + t) * NT + j) * kWave + lane] = acc[t][j];
+        __syncthreads();
+        for (int o = wave; o < RT * NT; o += waves) {  // a wavefront sums an output tile of a token tile
+            const int t = o / NT, j = o % NT;
+            float4_t v[NW];
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                v[k] = part[((k * RT + t) * NT + j) * kWave + lane];
+                for (int u = 1; u < waves; ++u) v[k] += part[((u * TILES + k * RT + t) * NT + j) * kWave + lane];
+            }
+            const int row = it.m0 + 16 * t + r;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = 16 * j + 4 * q + k;
+                const float y = MODE == GLU ? situ(v[0][k], v[NW - 1][k]) : v[0][k];
+                if (tok < it.n_tok && row < a.rows) store_out(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, y);
+            }
+        }
+        __syncthreads();  // part is read before the next item writes it
+    }
+}
+
+template <int XT, int GROUP, int MODE, int RT, int NT>
+int launch_int4_stream(const I4Args &a, hipStream_t st) {
+    constexpr int TILES = RT * (MODE == GLU ? 2 : 1);
+    const int turns = (a.in / 32 + 4 * kI4Steps - 1) / (4 * kI4Steps), waves = turns < kI4Waves ? turns : kI4Waves;
+    const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 16 * NT - 1) / (16 * NT)
+                                        : (int64_t)a.T / (16 * NT) + (a.E < a.T ? a.E : a.T);
+    const int64_t items = ((int64_t)a.rows + 16 * RT - 1) / (16 * RT) * tiles;
+    const int64_t most = 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
+    size_t lds = (size_t)waves * TILES * NT * kWave * 16 + (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
+    const void *f = (const void *)int4_stream_kernel<XT, GROUP, MODE, RT, NT>;
+    if (lds > 65536 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+        return K3G_EHIP;
+    int4_stream_kernel<XT, GROUP, MODE, RT, NT><<<(unsigned)grid, waves * kWave, lds, st>>>(a);
+    return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+}
+
+template <int XT, int GROUP, int MODE>
+int launch_int4_mode(const I4Args &a, hipStream_t st) {
+    if (MODE == DENSE && a.T <= 16 && a.rows <= 16 * 256) return launch_int4_stream<XT, GROUP, MODE, 1, 1>(a, st);
+    constexpr int RT = MODE == GLU ? 1 : 2;
+    const int64_t n = MODE == DENSE ? a.T : (a.T + a.E - 1) / a.E;
+    if (n <= 16) return launch_int4_stream<XT, GROUP, MODE, RT, 1>(a, st);
+    if (n <= 32) return launch_int4_stream<XT, GROUP, MODE, RT, 2>(a, st);
+    return launch_int4_stream<XT, GROUP, MODE, RT, 4>(a, st);
+}
+
+template <int XT, int GROUP>
+int launch_int4_group(const I4Args &a, int mode, hipStream_t st) {
+    return mode == DENSE ? launch_int4_mode<XT, GROUP, DENSE>(a, st) : mode == GROUPED ? launch_int4_mode<XT, GROUP, GROUPED>(a, st) : launch_int4_mode<XT, GROUP, GLU>(a, st);
+}
+
+template <int XT>
+int launch_int4_type(const I4Args &a, int mode, int group, hipStream_t st) {
+    return group == 32 ? launch_int4_group<XT, 32>(a, mode, st) : group == 64 ? launch_int4_group<XT, 64>(a, mode, st) : launch_int4_group<XT, 128>(a, mode, st);
+}
+
+}  // namespace k3g

@@ -177,14 +177,14 @@ __device__ inline void store_h(const MmArgs &a, int64_t token, int group, const 
 struct Item {
     int e, p, n_tok, m0;  // expert, first row of y, rows, first output
 };
-template <int MODE, int BN, int OUT>
+template <int MODE, int BN, int OUT, class Args = MmArgs>
 struct Items {
-    const MmArgs &a;
+    const Args &a;
     const int32_t *table;
     int n_rb, n_tiles, step, near = 0;  // near: an expert at or before the next item's
     int64_t item, last;
 
-    __device__ inline Items(const MmArgs &a_, int32_t *t, int threads) : a(a_), table(t) {
+    __device__ inline Items(const Args &a_, int32_t *t, int threads) : a(a_), table(t) {
         n_rb = (a.rows + OUT - 1) / OUT;
         if constexpr (MODE == DENSE) {
             n_tiles = (a.T + BN - 1) / BN;
