@@ -32,6 +32,7 @@ struct I4Args {
     int rows, in, G;         // outputs; entries and groups of a row
     int E, top_k;
     int s_type, y_type;
+    int x_vec;  // the rows of x lie at 16-byte addresses
 };
 
 // Eight codes (a dword, the low nibble first) as bf16 or fp16, in order. A code

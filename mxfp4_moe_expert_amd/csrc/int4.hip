@@ -26,7 +26,8 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
     return K3G_OK;
 }
 
-int launch(const I4Args &a, int mode, int x_type, int group, void *stream) {
+int launch(I4Args &a, int mode, int x_type, int group, void *stream) {
+    a.x_vec = mx_aligned(a.x, 16) && (a.xs * type_size(x_type) % 16 == 0 || a.x_rows == 1);
     hipStream_t st = (hipStream_t)stream;
     return x_type == K3G_F32    ? launch_int4_f32(a, mode, group, st)
            : x_type == K3G_BF16 ? launch_int4_bf16(a, mode, group, st)

@@ -1,0 +1,241 @@
+// int4_tile.h -- int4 products of many tokens: a workgroup takes 16 NJ rows of
+// activations and 64 outputs a wavefront (GLU: 32 of each weight), four
+// wavefronts. The activations come through LDS in steps of 128 columns, two
+// steps' places; each wavefront loads its own codes a step ahead and makes operands
+// of them in registers, once for all of the tile's tokens.
+#pragma once
+
+#include "int4_stream.h"
+
+namespace k3g {
+
+// Eight codes less their zero as bf16 or fp16, in order: z4 is the zero in each byte.
+// The subtraction is on whole bytes (of n + 128, so that none borrows from the
+// next), the conversion one instruction an entry that reads a byte with its sign, and
+// the fp32 result's upper half is the bf16. 19 instructions; against codes8 it spares
+// the product with ones and the multiplication of every partial sum, which a
+// tile of this many tokens would spend more on.
+template <int XT>
+__device__ inline uint4 codes8(uint32_t d, uint32_t z4) {
+    uint32_t lo = ((d & 0x0F0F0F0Fu) | 0x80808080u) - z4, hi = (((d >> 4) & 0x0F0F0F0Fu) | 0x80808080u) - z4;
+    lo ^= 0x80808080u, hi ^= 0x80808080u;
+    uint32_t v[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float e = (float)(int)(int8_t)(lo >> (8 * b)), o = (float)(int)(int8_t)(hi >> (8 * b));
+        if constexpr (XT == K3G_F16)
+            v[b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(e, o));
+        else
+            v[b] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, o), __builtin_bit_cast(uint32_t, e), 0x07060302u);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Global -> LDS without registers, 16 bytes a lane, each from its own address, to `lds` + 16 * lane.
+__device__ inline void dma16_from(const void *p, uint32_t lds) {
+    lds = __builtin_amdgcn_readfirstlane(lds);
+    __asm__ volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds) : "m0", "memory");
+}
+
+template <int XT, int NJ>
+constexpr int i4_step_bytes() { return (XT == K3G_F32 ? 3 : 1) * 16 * NJ * 256; }  // a step of the activations in LDS
+template <int GROUP>
+constexpr int i4_scale_bytes() { return 256 * (256 / GROUP) * 5; }  // 256 columns' scales and zeros of 256 weight rows
+
+template <int XT, int GROUP, int MODE, int NJ, bool DMA>
+__global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
+    constexpr int NW = MODE == GLU ? 2 : 1, TILES = 4, RT = TILES / NW, OUT = 4 * 16 * RT;
+    constexpr int SPAN = GROUP < 64 ? 1 : 2;  // blocks of 32 columns between two additions to the accumulators
+    constexpr int NG = 256 / GROUP;           // groups of a turn of two steps
+    constexpr int PLANES = XT == K3G_F32 ? 3 : 1, TOK = 16 * NJ, STEP = i4_step_bytes<XT, NJ>();
+    constexpr int X = XT == K3G_F32 ? 4 : 2, PARTS = TOK * 16 / 256;  // chunks of eight columns that a thread stages
+    static_assert(!DMA || PLANES == 1, "fp32 rows are split on the way");
+    extern __shared__ __align__(16) uint8_t lds[];
+    uint8_t *stage = lds;  // [2][plane][token][16 chunks of 8 columns, chunk c at c ^ (token % 16)]
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    float *scales = (float *)(lds + 2 * STEP) + wave * NG * kWave;                      // [group][weight row] of the wavefront
+    uint8_t *zeros = lds + 2 * STEP + 4 * NG * 256 + wave * NG * kWave;                 // the same
+    const uint8_t **src = (const uint8_t **)(lds + 2 * STEP + i4_scale_bytes<GROUP>());  // the tokens' rows
+    int32_t *table = (int32_t *)(src + TOK);
+    const int r = lane & 15, q = lane >> 4, lr = lane >> 2, lq = lane & 3, psrc = 4 * (4 * r + q);
+    const int units = a.in / 32, pitch = a.in / 2, S = (units + 3) / 4;
+    Items<MODE, TOK, OUT, I4Args> items(a, table, 256);
+    Item it;
+    while (items.next(it)) {
+        if (tid < TOK)
+            src[tid] = (const uint8_t *)a.x + X * ((int64_t)source(a, it.p + min(tid, it.n_tok - 1)) * a.xs);
+        // the wavefront's outputs from m on; its weight rows are 16 of tile 0, then of tile 1 ..
+        const int m = it.m0 + wave * 16 * RT, left = a.rows - 1 - m;
+        const int64_t first = (int64_t)it.e * a.rows + min(m, a.rows - 1);
+        uint32_t at[TILES];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) at[t] = (uint32_t)(max(min(16 * (t % RT) + lr, left), 0) * pitch);
+        const uint8_t *w0 = a.w[0] + first * pitch, *w1 = a.w[NW - 1] + first * pitch;
+        const int own = lane / (16 * RT);  // the weight whose scales this lane brings
+        const int64_t own_row = (first + max(min(lane % (16 * RT), left), 0)) * a.G;
+        const int nf = (it.n_tok + 15) / 16;
+        float4_t acc[TILES][NJ];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+        uint4 w[TILES], xr[DMA ? 1 : PARTS][XT == K3G_F32 ? 2 : 1];
+        float s[NG];
+        uint8_t z[NG];
+        auto load_w = [&](int step) {
+            const uint32_t c = 16u * (uint32_t)min(4 * step + lq, units - 1);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) w[t] = load16((t < RT ? w0 : w1) + (at[t] + c));
+        };
+        auto load_s = [&](int turn) {
+            const void *sp = a.s[NW == 2 ? own : 0];
+            const uint8_t *zp = a.z[NW == 2 ? own : 0];
+            const int g0 = turn * NG;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) z[g] = 8;
+            if (g0 + NG <= a.G) {
+                scales_at<NG>(s, sp, a.s_type, own_row + g0);
+                if (zp) __builtin_memcpy(z, zp + own_row + g0, NG);
+            } else {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int64_t i = own_row + min(g0 + g, a.G - 1);
+                    s[g] = scale_at(sp, a.s_type, i);
+                    if (zp) z[g] = zp[i];
+                }
+            }
+        };
+        // chunk tid % 16 of every 16th row from tid / 16 on
+        auto load_x = [&](int step) {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const int tok = tid / 16 + 16 * i, c = (tid & 15) ^ (tok & 15);
+                const uint8_t *p = src[tok] + X * 8 * (int64_t)min(16 * step + c, 4 * units - 1);
+                if constexpr (DMA)
+                    dma16_from(p, lds_addr(stage + (step & 1) * STEP + (4 * wave + 16 * i) * 256));
+                else
+                    __builtin_memcpy(xr[i], p, 8 * X);
+            }
+        };
+        auto put_x = [&](int step) {
+            if constexpr (!DMA) {
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    uint8_t *to = stage + (step & 1) * STEP + 16 * tid + 16 * 256 * i;
+                    if constexpr (XT == K3G_F32) {
+                        Act4<XT> v;
+                        v.load(xr[i]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) *(uint4 *)(to + k * TOK * 256) = v.part[k];
+                    } else {
+                        *(uint4 *)to = xr[i][0];
+                    }
+                }
+            }
+        };
+        __syncthreads();  // src; and the stages are free
+        load_s(0);
+        load_w(0);
+        load_x(0);
+        for (int step = 0; step < S; ++step) {
+            put_x(step);
+            if constexpr (DMA) wait_vm<0>();
+            if (step % 2 == 0) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    scales[g * kWave + lane] = s[g];
+                    zeros[g * kWave + lane] = z[g];
+                }
+            }
+            // this step's codes in operand order, before the registers are loaded again
+            uint32_t d[TILES][4];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                const uint4 v = to_operand(w[t], psrc);
+                d[t][0] = v.x, d[t][1] = v.y, d[t][2] = v.z, d[t][3] = v.w;
+                transpose4(d[t]);
+            }
+            __syncthreads();
+            if (step + 1 < S) {
+                if (step % 2 == 0 && step + 2 < S) load_s(step / 2 + 1);
+                load_w(step + 1);
+                load_x(step + 1);
+            }
+            const uint8_t *x0 = stage + (step & 1) * STEP + r * 256;
+#pragma unroll
+            for (int b = 0; b < 4; b += SPAN) {
+                if (4 * step + b < units) {
+                    const int g = (128 * (step & 1) + 32 * b) / GROUP;
+                    uint4 codes[TILES][SPAN];
+                    float sc[TILES];
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) {
+                        sc[t] = scales[g * kWave + 16 * t + r];
+                        const uint32_t z4 = zeros[g * kWave + 16 * t + r] * 0x01010101u;
+#pragma unroll
+                        for (int k = 0; k < SPAN; ++k) codes[t][k] = codes8<XT>(d[t][b + k], z4);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        if (j < nf) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            float4_t p[TILES];
+#pragma unroll
+                            for (int t = 0; t < TILES; ++t) p[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int k = 0; k < SPAN; ++k) {
+                                Act4<XT> x;
+                                const uint8_t *xp = x0 + j * 16 * 256 + 16 * ((4 * (b + k) + q) ^ r);
+                                if constexpr (XT == K3G_F32) {
+#pragma unroll
+                                    for (int n = 0; n < 3; ++n) x.part[n] = *(const uint4 *)(xp + n * TOK * 256);
+                                } else {
+                                    x.v = *(const uint4 *)xp;
+                                }
+#pragma unroll
+                                for (int t = 0; t < TILES; ++t) p[t] = x.mul(codes[t][k], p[t]);
+                            }
+#pragma unroll
+                            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[t][j][i] = __builtin_fmaf(sc[t], p[t][i], acc[t][j][i]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            if (j < nf) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int row = m + 16 * t + r;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * j + 4 * q + i;
+                        const float y = MODE == GLU ? situ(acc[t][j][i], acc[TILES - RT + t][j][i]) : acc[t][j][i];
+                        if (tok < it.n_tok && row < a.rows) store_out(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, y);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the stages and src are read before the next item writes them
+    }
+}
+
+template <int XT, int GROUP, int MODE, int NJ, bool DMA>
+int launch_int4_tile(const I4Args &a, hipStream_t st) {
+    constexpr int OUT = MODE == GLU ? 128 : 256, TOK = 16 * NJ;
+    const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + TOK - 1) / TOK : (int64_t)a.T / TOK + (a.E < a.T ? a.E : a.T);
+    const int64_t items = ((int64_t)a.rows + OUT - 1) / OUT * tiles;
+    const int64_t most = 512, grid = items < most ? (items + 7) / 8 * 8 : most;
+    const size_t lds = 2 * (size_t)i4_step_bytes<XT, NJ>() + i4_scale_bytes<GROUP>() + 8 * TOK +
+                       (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
+    const void *f = (const void *)int4_tile_kernel<XT, GROUP, MODE, NJ, DMA>;
+    if (lds > 65536 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+        return K3G_EHIP;
+    int4_tile_kernel<XT, GROUP, MODE, NJ, DMA><<<(unsigned)grid, 256, lds, st>>>(a);
+    return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+}
+
+}  // namespace k3g

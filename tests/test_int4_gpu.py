@@ -49,11 +49,12 @@ def test_whole_numbers_are_exact(k3g, T, n, rows, group, xt):
         for st in TYPES:
             w = ref.random_weights(g, (rows,), n, group, st, zeros, exact=True)
             x = ref.rows_of(g, T, n, xt, exact=True)
-            b, y = output(T, rows, torch.float32)
-            k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
             want = x.double() @ ref.values(*w)[0].t().contiguous()
-            assert torch.equal(y.double(), want), (zeros, st)
-            assert untouched(b, T, rows)
+            for a in (x, x.clone()):  # rows off 16-byte addresses, and on them
+                b, y = output(T, rows, torch.float32)
+                k3g.k3g_int4_matmul(y, a, k3g.int4(*w))
+                assert torch.equal(y.double(), want), (zeros, st)
+                assert untouched(b, T, rows)
 
 
 @pytest.mark.parametrize("xt", TYPES, ids=name)
@@ -64,6 +65,8 @@ def test_values(k3g, T, n, rows, group, xt, yt):
     for st, zeros in ((torch.bfloat16, False), (torch.float16, True), (torch.float32, True)):
         w = ref.random_weights(g, (rows,), n, group, st, zeros)
         x = ref.rows_of(g, T, n, xt, pad=5)
+        if zeros:
+            x = x.contiguous()
         b, y = output(T, rows, yt, pad=3)
         k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
         m, mag = ref.values(*w)
