@@ -139,9 +139,23 @@ __device__ inline int source(const I4Args &a, int p) {
     return min((int)((unsigned)max(q, 0) / (unsigned)a.top_k), a.x_rows - 1);
 }
 
-// int4_{f32,bf16,f16}.hip: a product's launch for activations of one type
-int launch_int4_f32(const I4Args &a, int mode, int group, hipStream_t st);
-int launch_int4_bf16(const I4Args &a, int mode, int group, hipStream_t st);
-int launch_int4_f16(const I4Args &a, int mode, int group, hipStream_t st);
+// v[c] of lane row q <-> v[q] of lane row c (a lane row: 16 lanes).
+__device__ inline void transpose4(uint32_t *v) {
+    auto s = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    auto t = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    auto a = __builtin_amdgcn_permlane16_swap(s[0], t[0], false, false);
+    auto b = __builtin_amdgcn_permlane16_swap(s[1], t[1], false, false);
+    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+}
+
+// A product's launch: int4_gemv.hip, int4_stream_{f32,bf16,f16}.hip, int4_tile_{f32,bf16,f16}.hip
+constexpr int kGvMaxIn = 32768;
+int launch_int4_gemv(const I4Args &a, int mode, int x_type, int group, hipStream_t st);
+int launch_int4_stream_f32(const I4Args &a, int mode, int group, int form, hipStream_t st);
+int launch_int4_stream_bf16(const I4Args &a, int mode, int group, int form, hipStream_t st);
+int launch_int4_stream_f16(const I4Args &a, int mode, int group, int form, hipStream_t st);
+int launch_int4_tile_f32(const I4Args &a, int mode, int group, int form, hipStream_t st);
+int launch_int4_tile_bf16(const I4Args &a, int mode, int group, int form, hipStream_t st);
+int launch_int4_tile_f16(const I4Args &a, int mode, int group, int form, hipStream_t st);
 
 }  // namespace k3g

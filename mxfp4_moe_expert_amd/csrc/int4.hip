@@ -26,12 +26,27 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
     return K3G_OK;
 }
 
+// The kernel of a product: weight rows << 16 | tokens of its tile; a single row's has one token.
+int product_form(const I4Args &a, int mode, int x_type) {
+    if (a.in <= kGvMaxIn && (a.T == 1 || (mode != DENSE && a.T <= 64 && 2 * a.T <= a.E))) return form(8, 1);
+    const int64_t n = mode == DENSE ? a.T : ((int64_t)a.T + a.E - 1) / a.E;
+    if (n > 32) return x_type != K3G_F32 && a.x_vec ? form(256, 128) : form(256, 64);
+    if (mode == DENSE && a.T <= 16 && a.rows <= 16 * 256) return form(16, 16);
+    return n <= 16 ? form(32, 16) : form(32, 32);
+}
+
 int launch(I4Args &a, int mode, int x_type, int group, void *stream) {
-    a.x_vec = mx_aligned(a.x, 16) && (a.xs * type_size(x_type) % 16 == 0 || a.x_rows == 1);
     hipStream_t st = (hipStream_t)stream;
-    return x_type == K3G_F32    ? launch_int4_f32(a, mode, group, st)
-           : x_type == K3G_BF16 ? launch_int4_bf16(a, mode, group, st)
-                                : launch_int4_f16(a, mode, group, st);
+    a.x_vec = mx_aligned(a.x, 16) && (a.xs * type_size(x_type) % 16 == 0 || a.x_rows == 1);
+    const int f = product_form(a, mode, x_type);
+    if (f == form(8, 1)) return launch_int4_gemv(a, mode, x_type, group, st);
+    if (f >> 16 <= 32)
+        return x_type == K3G_F32    ? launch_int4_stream_f32(a, mode, group, f, st)
+               : x_type == K3G_BF16 ? launch_int4_stream_bf16(a, mode, group, f, st)
+                                    : launch_int4_stream_f16(a, mode, group, f, st);
+    return x_type == K3G_F32    ? launch_int4_tile_f32(a, mode, group, f, st)
+           : x_type == K3G_BF16 ? launch_int4_tile_bf16(a, mode, group, f, st)
+                                : launch_int4_tile_f16(a, mode, group, f, st);
 }
 
 // The grouped calls' checks of everything but the weights; n_w spans of those in `use`.

@@ -20,15 +20,6 @@ namespace k3g {
 constexpr int kI4Steps = 4;  // steps of 128 columns that a wavefront loads together
 constexpr int kI4Waves = 8;
 
-// v[c] of lane row q <-> v[q] of lane row c (a lane row: 16 lanes).
-__device__ inline void transpose4(uint32_t *v) {
-    auto s = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-    auto t = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-    auto a = __builtin_amdgcn_permlane16_swap(s[0], t[0], false, false);
-    auto b = __builtin_amdgcn_permlane16_swap(s[1], t[1], false, false);
-    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
-}
-
 template <int XT, int GROUP, int MODE, int RT, int NT>
 __global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a) {
     constexpr int NW = MODE == GLU ? 2 : 1, TILES = RT * NW, BLOCKS = GROUP / 32;
@@ -174,6 +165,28 @@ int launch_int4_stream(const I4Args &a, hipStream_t st) {
         return K3G_EHIP;
     int4_stream_kernel<XT, GROUP, MODE, RT, NT><<<(unsigned)grid, waves * kWave, lds, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+}
+
+template <int XT, int GROUP, int MODE>
+int launch_int4_stream_form(const I4Args &a, int f, hipStream_t st) {
+    constexpr int NW = MODE == GLU ? 2 : 1;
+    if (MODE == DENSE && f == form(16, 16)) return launch_int4_stream<XT, GROUP, MODE, 1, 1>(a, st);
+    if (f == form(32, 16)) return launch_int4_stream<XT, GROUP, MODE, 2 / NW, 1>(a, st);
+    return launch_int4_stream<XT, GROUP, MODE, 2 / NW, 2>(a, st);
+}
+
+template <int XT, int GROUP>
+int launch_int4_stream_mode(const I4Args &a, int mode, int f, hipStream_t st) {
+    return mode == DENSE     ? launch_int4_stream_form<XT, GROUP, DENSE>(a, f, st)
+           : mode == GROUPED ? launch_int4_stream_form<XT, GROUP, GROUPED>(a, f, st)
+                             : launch_int4_stream_form<XT, GROUP, GLU>(a, f, st);
+}
+
+template <int XT>
+int launch_int4_stream_type(const I4Args &a, int mode, int group, int f, hipStream_t st) {
+    return group == 32   ? launch_int4_stream_mode<XT, 32>(a, mode, f, st)
+           : group == 64 ? launch_int4_stream_mode<XT, 64>(a, mode, f, st)
+                         : launch_int4_stream_mode<XT, 128>(a, mode, f, st);
 }
 
 }  // namespace k3g

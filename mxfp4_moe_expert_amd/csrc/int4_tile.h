@@ -5,7 +5,7 @@
 // of them in registers, once for all of the tile's tokens.
 #pragma once
 
-#include "int4_stream.h"
+#include "int4.h"
 
 namespace k3g {
 
@@ -158,7 +158,6 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             __syncthreads();
             if (step + 1 < S) {
                 if (step % 2 == 0 && step + 2 < S) load_s(step / 2 + 1);
-                load_w(step + 1);
                 load_x(step + 1);
             }
             const uint8_t *x0 = stage + (step & 1) * STEP + r * 256;
@@ -166,6 +165,19 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             for (int b = 0; b < 4; b += SPAN) {
                 if (4 * step + b < units) {
                     const int g = (128 * (step & 1) + 32 * b) / GROUP;
+                    Act4<XT> x[2][SPAN];
+                    auto read_x = [&](int j) {
+#pragma unroll
+                        for (int k = 0; k < SPAN; ++k) {
+                            const uint8_t *xp = x0 + j * 16 * 256 + 16 * ((4 * (b + k) + q) ^ r);
+                            if constexpr (XT == K3G_F32) {
+#pragma unroll
+                                for (int n = 0; n < 3; ++n) x[j & 1][k].part[n] = *(const uint4 *)(xp + n * TOK * 256);
+                            } else {
+                                x[j & 1][k].v = *(const uint4 *)xp;
+                            }
+                        }
+                    };
                     uint4 codes[TILES][SPAN];
                     float sc[TILES];
 #pragma unroll
@@ -175,33 +187,34 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
 #pragma unroll
                         for (int k = 0; k < SPAN; ++k) codes[t][k] = codes8<XT>(d[t][b + k], z4);
                     }
+                    // two token tiles at a time: the products of the second run as the sums of the first are added
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        if (j < nf) {
-                            __builtin_amdgcn_sched_barrier(0);
-                            float4_t p[TILES];
+                    for (int j0 = 0; j0 < NJ; j0 += 2) {
+                        if (j0 < nf) {
+                            float4_t p[2][TILES];
 #pragma unroll
-                            for (int t = 0; t < TILES; ++t) p[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+                            for (int h = 0; h < 2; ++h) read_x(j0 + h);
 #pragma unroll
-                            for (int k = 0; k < SPAN; ++k) {
-                                Act4<XT> x;
-                                const uint8_t *xp = x0 + j * 16 * 256 + 16 * ((4 * (b + k) + q) ^ r);
-                                if constexpr (XT == K3G_F32) {
+                            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                                    for (int n = 0; n < 3; ++n) x.part[n] = *(const uint4 *)(xp + n * TOK * 256);
-                                } else {
-                                    x.v = *(const uint4 *)xp;
-                                }
+                                for (int t = 0; t < TILES; ++t)
+                                    p[h][t] = x[h][0].mul(codes[t][0], float4_t{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                                for (int t = 0; t < TILES; ++t) p[t] = x.mul(codes[t][k], p[t]);
+                                for (int k = 1; k < SPAN; ++k)
+#pragma unroll
+                                    for (int t = 0; t < TILES; ++t) p[h][t] = x[h][k].mul(codes[t][k], p[h][t]);
                             }
 #pragma unroll
-                            for (int t = 0; t < TILES; ++t)
+                            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) acc[t][j][i] = __builtin_fmaf(sc[t], p[t][i], acc[t][j][i]);
+                                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        acc[t][j0 + h][i] = __builtin_fmaf(sc[t], p[h][t][i], acc[t][j0 + h][i]);
                         }
                     }
                 }
+                if (b == 4 - 2 * SPAN && step + 1 < S) load_w(step + 1);
             }
         }
 #pragma unroll
@@ -236,6 +249,27 @@ int launch_int4_tile(const I4Args &a, hipStream_t st) {
         return K3G_EHIP;
     int4_tile_kernel<XT, GROUP, MODE, NJ, DMA><<<(unsigned)grid, 256, lds, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+}
+
+template <int XT, int GROUP, int MODE>
+int launch_int4_tile_form(const I4Args &a, int f, hipStream_t st) {
+    if constexpr (XT != K3G_F32)
+        if (f == form(256, 128)) return launch_int4_tile<XT, GROUP, MODE, 8, true>(a, st);
+    return launch_int4_tile<XT, GROUP, MODE, 4, false>(a, st);
+}
+
+template <int XT, int GROUP>
+int launch_int4_tile_mode(const I4Args &a, int mode, int f, hipStream_t st) {
+    return mode == DENSE     ? launch_int4_tile_form<XT, GROUP, DENSE>(a, f, st)
+           : mode == GROUPED ? launch_int4_tile_form<XT, GROUP, GROUPED>(a, f, st)
+                             : launch_int4_tile_form<XT, GROUP, GLU>(a, f, st);
+}
+
+template <int XT>
+int launch_int4_tile_type(const I4Args &a, int mode, int group, int f, hipStream_t st) {
+    return group == 32   ? launch_int4_tile_mode<XT, 32>(a, mode, f, st)
+           : group == 64 ? launch_int4_tile_mode<XT, 64>(a, mode, f, st)
+                         : launch_int4_tile_mode<XT, 128>(a, mode, f, st);
 }
 
 }  // namespace k3g

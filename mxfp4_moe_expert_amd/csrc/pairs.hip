@@ -241,9 +241,9 @@ __device__ inline void store_cols(void *base, int64_t at, int n, const float *v)
 // SCATTER: sorted rows are written from the token's row. SUM: the sorted rows are
 // summed into the token's. DOT: their products with the token's row are summed.
 // An item: a token, a part of its columns and (no SUM) some of its pairs; DOT
-// takes all columns. Four sorted rows are loaded at a time.
-template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT>
-__global__ __launch_bounds__(1024) void pairs_kernel(PairArgs a) {
+// takes all columns. U sorted rows are loaded at a time.
+template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT, int U>
+__global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
     __shared__ float part[DOT ? 16 * kPairMaxTopK : 1];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int turns = (a.K + a.slots - 1) / a.slots, width = a.waves * kWave * kPairCols;
@@ -259,22 +259,22 @@ __global__ __launch_bounds__(1024) void pairs_kernel(PairArgs a) {
             const int c = c0 + tid * kPairCols, n = a.n - c;
             float tok[kPairCols], sum[kPairCols] = {};
             if (SCATTER || DOT) load_cols<TOK>(tok, a.tok, n > 0 ? t * a.tok_ld + c : 0, n);
-            for (int k = k0; k < k1; k += 4) {
-                int p[4];
-                float w[4], v[4][kPairCols];
+            for (int k = k0; k < k1; k += U) {
+                int p[U];
+                float w[U], v[U][kPairCols];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < U; ++j) {
                     p[j] = k + j < k1 ? inv[k + j] : -1;
                     if ((unsigned)p[j] >= (unsigned)a.R) p[j] = -1;
                     if (SCATTER || SUM) w[j] = a.wts && p[j] >= 0 ? a.wts[t * a.K + k + j] : 1.0f;
                 }
                 if (SUM || DOT) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < U; ++j)
                         if (p[j] >= 0) load_cols<ROW>(v[j], a.row, n > 0 ? p[j] * a.row_ld + c : 0, n);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < U; ++j) {
                     if (p[j] < 0) continue;
                     if (SUM) {
 #pragma unroll
@@ -320,8 +320,15 @@ int launch_pairs(PairArgs a, hipStream_t st) {
         a.waves = row_waves < 8 ? row_waves : 8;
         a.parts = (row_waves + a.waves - 1) / a.waves;
     }
+    if (SUM && !DOT && (int64_t)a.T * a.parts * a.waves < 4096) {  // few tokens: all of their rows at once
+        a.parts = row_waves;
+        a.waves = 1;
+        const int64_t items = (int64_t)a.T * a.parts;
+        pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, 16><<<(unsigned)items, kWave, 0, st>>>(a);
+        return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+    }
     const int64_t items = (int64_t)a.T * a.parts * ((a.K + a.slots - 1) / a.slots), most = 1 << 20;
-    pairs_kernel<ROW, TOK, SCATTER, SUM, DOT>
+    pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, 4>
         <<<(unsigned)(items < most ? items : most), a.waves * kWave, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
