@@ -55,14 +55,26 @@ __device__ inline uint4 codes8(uint32_t d) {
                           __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true)));
 }
 
-// Eight entries of a token as operand A. fp32 goes in as three bf16 parts whose
-// sum it is: each the leading 8 bits of what the ones before leave.
+// Eight entries of a token as they lie in memory.
+template <int XT>
+struct Raw4 {
+    uint4 v;
+    __device__ inline void load(const void *p) { __builtin_memcpy(&v, p, 16); }
+};
+template <>
+struct Raw4<K3G_F32> {
+    float f[8];
+    __device__ inline void load(const void *p) { __builtin_memcpy(f, p, 32); }
+};
+
+// And as operand A. fp32 goes in as three bf16 parts whose sum it is: each the
+// leading 8 bits of what the ones before leave.
 template <int XT>
 struct Act4;
 template <>
 struct Act4<K3G_BF16> {
     uint4 v;
-    __device__ inline void load(const void *p) { __builtin_memcpy(&v, p, 16); }
+    __device__ inline void take(const Raw4<K3G_BF16> &x) { v = x.v; }
     __device__ inline float4_t mul(const uint4 &w, float4_t c) const {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, w), c, 0,
                                                        0, 0);
@@ -72,7 +84,7 @@ struct Act4<K3G_BF16> {
 template <>
 struct Act4<K3G_F16> {
     uint4 v;
-    __device__ inline void load(const void *p) { __builtin_memcpy(&v, p, 16); }
+    __device__ inline void take(const Raw4<K3G_F16> &x) { v = x.v; }
     __device__ inline float4_t mul(const uint4 &w, float4_t c) const {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, w), c, 0, 0,
                                                       0);
@@ -82,9 +94,10 @@ struct Act4<K3G_F16> {
 template <>
 struct Act4<K3G_F32> {
     uint4 part[3];
-    __device__ inline void load(const void *p) {
+    __device__ inline void take(const Raw4<K3G_F32> &x) {
         float f[8];
-        __builtin_memcpy(f, p, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = x.f[i];
         uint32_t d[3][4];
 #pragma unroll
         for (int k = 0; k < 3; ++k) {

@@ -30,9 +30,9 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 int product_form(const I4Args &a, int mode, int x_type) {
     if (a.in <= kGvMaxIn && (a.T == 1 || (mode != DENSE && a.T <= 64 && 2 * a.T <= a.E))) return form(8, 1);
     const int64_t n = mode == DENSE ? a.T : ((int64_t)a.T + a.E - 1) / a.E;
-    if (n > 32) return x_type != K3G_F32 && a.x_vec ? form(256, 128) : form(256, 64);
+    if (n > 64) return x_type != K3G_F32 && a.x_vec ? form(256, 128) : form(256, 64);
     if (mode == DENSE && a.T <= 16 && a.rows <= 16 * 256) return form(16, 16);
-    return n <= 16 ? form(32, 16) : form(32, 32);
+    return n <= 16 ? form(32, 16) : form(64, 32);
 }
 
 int launch(I4Args &a, int mode, int x_type, int group, void *stream) {
@@ -40,7 +40,7 @@ int launch(I4Args &a, int mode, int x_type, int group, void *stream) {
     a.x_vec = mx_aligned(a.x, 16) && (a.xs * type_size(x_type) % 16 == 0 || a.x_rows == 1);
     const int f = product_form(a, mode, x_type);
     if (f == form(8, 1)) return launch_int4_gemv(a, mode, x_type, group, st);
-    if (f >> 16 <= 32)
+    if (f >> 16 <= 64)
         return x_type == K3G_F32    ? launch_int4_stream_f32(a, mode, group, f, st)
                : x_type == K3G_BF16 ? launch_int4_stream_bf16(a, mode, group, f, st)
                                     : launch_int4_stream_f16(a, mode, group, f, st);

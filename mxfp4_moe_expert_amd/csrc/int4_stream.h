@@ -1,7 +1,7 @@
 // int4_stream.h -- int4 products whose weights are streamed once: a workgroup
 // takes 16 NT rows of activations and 16 RT outputs (of one expert) and splits
-// the row's length over its wavefronts, 512 columns at a time, whose codes and
-// scales are all in flight before the first product. The wavefronts' sums meet in
+// the row's length over its wavefronts, 512 columns at a time (256 of four tiles), whose
+// codes and scales are all in flight before the first product. The wavefronts' sums meet in
 // LDS and are added in wavefront order.
 //
 // Operand A is the activations (16 tokens), operand B the codes (16 outputs):
@@ -17,13 +17,16 @@
 
 namespace k3g {
 
-constexpr int kI4Steps = 4;  // steps of 128 columns that a wavefront loads together
 constexpr int kI4Waves = 8;
+constexpr int i4_stream_occupancy(int xt, int group, int tiles) { return tiles > 2 || xt == K3G_F32 ? 2 : group == 32 ? 3 : 4; }  // wavefronts a SIMD
+constexpr int i4_stream_steps(int tiles) { return tiles > 2 ? 2 : 4; }
 
 template <int XT, int GROUP, int MODE, int RT, int NT>
-__global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a) {
-    constexpr int NW = MODE == GLU ? 2 : 1, TILES = RT * NW, BLOCKS = GROUP / 32;
-    constexpr int NG = 128 * kI4Steps / GROUP;  // groups of a turn
+__global__ __launch_bounds__(kI4Waves * kWave, i4_stream_occupancy(XT, GROUP, RT * (MODE == GLU ? 2 : 1) * NT)) void int4_stream_kernel(I4Args a) {
+    constexpr int NW = MODE == GLU ? 2 : 1, TILES = RT * NW;
+    constexpr int STEPS = i4_stream_steps(TILES);                          // of 128 columns that are loaded together
+    constexpr int SPAN = XT == K3G_F32 || GROUP == 32 ? 1 : 2;             // blocks of 32 columns between two additions
+    constexpr int NG = 128 * STEPS / GROUP;                                // groups of a turn
     constexpr int X = XT == K3G_F32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int waves = blockDim.x / kWave;
@@ -37,15 +40,13 @@ __global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a)
     Items<MODE, 16 * NT, 16 * RT, I4Args> items(a, table, blockDim.x);
     Item it;
     while (items.next(it)) {
-        const uint8_t *wc[TILES], *zc[TILES];
-        int64_t sc[TILES];
+        const int64_t first = (int64_t)it.e * a.rows + it.m0;
+        uint32_t at[TILES];  // bytes from the first row's codes
+        int srow[TILES];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int k = t / RT, m = it.m0 + 16 * (t % RT);
-            const int64_t row = (int64_t)it.e * a.rows;
-            wc[t] = a.w[k] + (row + min(m + lr, a.rows - 1)) * pitch;
-            sc[t] = (row + min(m + r, a.rows - 1)) * a.G;
-            zc[t] = a.z[k] + sc[t];
+            at[t] = (uint32_t)(min(16 * (t % RT) + lr, a.rows - 1 - it.m0) * pitch);
+            srow[t] = min(16 * (t % RT) + r, a.rows - 1 - it.m0) * a.G;
         }
         const uint8_t *xc[NT];
 #pragma unroll
@@ -56,71 +57,86 @@ __global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a)
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-        for (int u0 = 4 * kI4Steps * wave; u0 < units; u0 += 4 * kI4Steps * waves) {
-            uint4 w[kI4Steps][TILES];
+        const int nf = (it.n_tok + 15) / 16;
+        for (int u0 = 4 * STEPS * wave; u0 < units; u0 += 4 * STEPS * waves) {
+            uint4 w[STEPS][TILES];
             float s[TILES][NG];
             uint8_t z[TILES][NG];
 #pragma unroll
-            for (int i = 0; i < kI4Steps; ++i)
+            for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) w[i][t] = load16(wc[t] + 16 * (int64_t)min(u0 + 4 * i + lq, units - 1));
-            const int g0 = u0 / BLOCKS;
+                for (int t = 0; t < TILES; ++t)
+                    w[i][t] = load16(a.w[t / RT] + first * pitch + (at[t] + 16u * (uint32_t)min(u0 + 4 * i + lq, units - 1)));
+            // raw entries of a token tile's span; of the next one while this one is used
+            Raw4<XT> x[2][NT][SPAN];
+            auto load_x = [&](int k) {
+#pragma unroll
+                for (int n = 0; n < SPAN; ++n)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        x[k & 1][j][n].load(xc[j] + X * 32 * (int64_t)min(u0 + SPAN * k + n, units - 1));
+            };
+            load_x(0);
+            const int g0 = u0 * 32 / GROUP;
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
                 const void *sp = a.s[t / RT];
+                const int64_t s0 = first * a.G + srow[t];
+                const uint8_t *zp = a.z[t / RT];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) z[t][g] = 8;
                 if (g0 + NG <= a.G) {
-                    scales_at<NG>(s[t], sp, a.s_type, sc[t] + g0);
-                    if (a.z[t / RT]) __builtin_memcpy(z[t], zc[t] + g0, NG);
+                    scales_at<NG>(s[t], sp, a.s_type, s0 + g0);
+                    if (zp) __builtin_memcpy(z[t], zp + s0 + g0, NG);
                 } else {
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const int at = min(g0 + g, a.G - 1);
-                        s[t][g] = scale_at(sp, a.s_type, sc[t] + at);
-                        if (a.z[t / RT]) z[t][g] = zc[t][at];
+                        const int64_t i = s0 + min(g0 + g, a.G - 1);
+                        s[t][g] = scale_at(sp, a.s_type, i);
+                        if (zp) z[t][g] = zp[i];
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kI4Steps; ++i) {
-                if (u0 + 4 * i >= units) break;
-                Act4<XT> x[NT][4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j][b].load(xc[j] + X * 32 * (int64_t)min(u0 + 4 * i + b, units - 1));
-                uint32_t d[TILES][4];
-#pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    const uint4 v = to_operand(w[i][t], psrc);
-                    d[t][0] = v.x, d[t][1] = v.y, d[t][2] = v.z, d[t][3] = v.w;
-                    transpose4(d[t]);
-                }
-#pragma unroll
-                for (int b = 0; b < 4; b += BLOCKS) {
-                    if (u0 + 4 * i + b >= units) break;
-                    const int g = (4 * i + b) / BLOCKS;
-                    float4_t sum[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        sum[j] = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) sum[j] = x[j][b + k].mul(Act4<XT>::ones(), sum[j]);
-                    }
+            for (int i = 0; i < STEPS; ++i) {
+                if (u0 + 4 * i < units) {
+                    uint32_t d[TILES][4];
 #pragma unroll
                     for (int t = 0; t < TILES; ++t) {
-                        uint4 codes[BLOCKS];
+                        const uint4 v = to_operand(w[i][t], psrc);
+                        d[t][0] = v.x, d[t][1] = v.y, d[t][2] = v.z, d[t][3] = v.w;
+                        transpose4(d[t]);
+                    }
 #pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) codes[k] = codes8<XT>(d[t][b + k]);
-                        const float zero = -(float)z[t][g];
+                    for (int b = 0; b < 4; b += SPAN) {
+                        if (u0 + 4 * i + b < units) {
+                            const int k = (4 * i + b) / SPAN, g = (4 * i + b) * 32 / GROUP;
+                            if (k + 1 < 4 * STEPS / SPAN) load_x(k + 1);
+                            uint4 codes[TILES][SPAN];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            float4_t p = zero * sum[j];
+                            for (int t = 0; t < TILES; ++t)
 #pragma unroll
-                            for (int k = 0; k < BLOCKS; ++k) p = x[j][b + k].mul(codes[k], p);
+                                for (int n = 0; n < SPAN; ++n) codes[t][n] = codes8<XT>(d[t][b + n]);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[t][j][k] = __builtin_fmaf(s[t][g], p[k], acc[t][j][k]);
+                            for (int j = 0; j < NT; ++j) {
+                                if (NT == 1 || j < nf) {
+                                    Act4<XT> v[SPAN];
+                                    float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                    for (int n = 0; n < SPAN; ++n) {
+                                        v[n].take(x[k & 1][j][n]);
+                                        sum = v[n].mul(Act4<XT>::ones(), sum);
+                                    }
+#pragma unroll
+                                    for (int t = 0; t < TILES; ++t) {
+                                        float4_t p = -(float)z[t][g] * sum;
+#pragma unroll
+                                        for (int n = 0; n < SPAN; ++n) p = v[n].mul(codes[t][n], p);
+#pragma unroll
+                                        for (int n = 0; n < 4; ++n) acc[t][j][n] = __builtin_fmaf(s[t][g], p[n], acc[t][j][n]);
+                                    }
+                                }
+                            }
                         }
                     }
                 }
@@ -154,11 +170,13 @@ __global__ __launch_bounds__(kI4Waves * kWave) void int4_stream_kernel(I4Args a)
 template <int XT, int GROUP, int MODE, int RT, int NT>
 int launch_int4_stream(const I4Args &a, hipStream_t st) {
     constexpr int TILES = RT * (MODE == GLU ? 2 : 1);
-    const int turns = (a.in / 32 + 4 * kI4Steps - 1) / (4 * kI4Steps), waves = turns < kI4Waves ? turns : kI4Waves;
+    const int turns = (a.in / 32 + 4 * i4_stream_steps(TILES) - 1) / (4 * i4_stream_steps(TILES));
     const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 16 * NT - 1) / (16 * NT)
                                         : (int64_t)a.T / (16 * NT) + (a.E < a.T ? a.E : a.T);
     const int64_t items = ((int64_t)a.rows + 16 * RT - 1) / (16 * RT) * tiles;
-    const int64_t most = 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
+    const bool alone = items >= 8192;
+    const int waves = alone ? 1 : turns < kI4Waves ? turns : kI4Waves;
+    const int64_t most = alone ? 4096 : 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
     size_t lds = (size_t)waves * TILES * NT * kWave * 16 + (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
     const void *f = (const void *)int4_stream_kernel<XT, GROUP, MODE, RT, NT>;
     if (lds > 65536 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
@@ -170,9 +188,10 @@ int launch_int4_stream(const I4Args &a, hipStream_t st) {
 template <int XT, int GROUP, int MODE>
 int launch_int4_stream_form(const I4Args &a, int f, hipStream_t st) {
     constexpr int NW = MODE == GLU ? 2 : 1;
-    if (MODE == DENSE && f == form(16, 16)) return launch_int4_stream<XT, GROUP, MODE, 1, 1>(a, st);
+    if constexpr (MODE == DENSE)
+        if (f == form(16, 16)) return launch_int4_stream<XT, GROUP, MODE, 1, 1>(a, st);
     if (f == form(32, 16)) return launch_int4_stream<XT, GROUP, MODE, 2 / NW, 1>(a, st);
-    return launch_int4_stream<XT, GROUP, MODE, 2 / NW, 2>(a, st);
+    return launch_int4_stream<XT, GROUP, MODE, 4 / NW, 2>(a, st);
 }
 
 template <int XT, int GROUP>

@@ -79,7 +79,8 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-        uint4 w[TILES], xr[DMA ? 1 : PARTS][XT == K3G_F32 ? 2 : 1];
+        uint4 w[TILES];
+        Raw4<XT> xr[DMA ? 1 : PARTS];
         float s[NG];
         uint8_t z[NG];
         auto load_w = [&](int step) {
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
                 if constexpr (DMA)
                     dma16_from(p, lds_addr(stage + (step & 1) * STEP + (4 * wave + 16 * i) * 256));
                 else
-                    __builtin_memcpy(xr[i], p, 8 * X);
+                    xr[i].load(p);
             }
         };
         auto put_x = [&](int step) {
@@ -124,11 +125,11 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
                     uint8_t *to = stage + (step & 1) * STEP + 16 * tid + 16 * 256 * i;
                     if constexpr (XT == K3G_F32) {
                         Act4<XT> v;
-                        v.load(xr[i]);
+                        v.take(xr[i]);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) *(uint4 *)(to + k * TOK * 256) = v.part[k];
                     } else {
-                        *(uint4 *)to = xr[i][0];
+                        *(uint4 *)to = xr[i].v;
                     }
                 }
             }
