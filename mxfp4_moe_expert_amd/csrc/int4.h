@@ -145,6 +145,28 @@ __device__ inline void store_out(void *y, int type, int64_t i, float v) {
         ((_Float16 *)y)[i] = (_Float16)v;
 }
 
+// N consecutive outputs, of which the first n are there.
+template <int N, int TYPE>
+__device__ inline void store_outs_as(void *y, int64_t i, int n, const float *v) {
+    typename Elem<TYPE>::T *p = (typename Elem<TYPE>::T *)y + i;
+    if (n >= N) {
+        store_n<TYPE, N>(p, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < n) p[k] = Elem<TYPE>::store(v[k]);
+    }
+}
+template <int N>
+__device__ inline void store_outs(void *y, int type, int64_t i, int n, const float *v) {
+    if (type == K3G_F32)
+        store_outs_as<N, K3G_F32>(y, i, n, v);
+    else if (type == K3G_BF16)
+        store_outs_as<N, K3G_BF16>(y, i, n, v);
+    else
+        store_outs_as<N, K3G_F16>(y, i, n, v);
+}
+
 // The source row of row p of y.
 __device__ inline int source(const I4Args &a, int p) {
     if (!a.perm) return p;
