@@ -678,18 +678,29 @@ def k3g_mx_grouped_glu(h: Mx, a: Mx, bank: ExpertBank, offsets: torch.Tensor, pe
 
 # ---- routed pairs -------------------------------------------------------------
 
+def _flat(t: torch.Tensor, dtype, name: str) -> int:
+    """A contiguous device tensor of that type; returns its device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must live on the GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return d
+
+
 def k3g_moe_sort(offsets: torch.Tensor, perm: torch.Tensor, inv: torch.Tensor, idx: torch.Tensor, ws: torch.Tensor,
                  stream=None):
     """The pairs of idx [T, K] sorted by expert, stably: offsets [n_experts + 1], perm [T * K] (sorted row -> pair
     t * K + k, -1 behind the last) and inv [T, K] (pair -> sorted row, -1 for an id outside the experts). ws:
     workspace(OP_MOE_SORT, shape(n_tokens, top_k, n_experts)). Returns (offsets, perm, inv)."""
-    for name, t in (("offsets", offsets), ("perm", perm), ("inv", inv), ("idx", idx)):
-        _dev(t, torch.int32, name)
-    _dev(ws, torch.uint8, "ws")
+    devices = (_flat(offsets, torch.int32, "offsets"), _flat(perm, torch.int32, "perm"), _flat(inv, torch.int32, "inv"),
+               _flat(idx, torch.int32, "idx"), _flat(ws, torch.uint8, "ws"))
     if idx.dim() != 2 or inv.shape != idx.shape or perm.numel() != idx.numel() or offsets.numel() < 2:
         raise ValueError("shape mismatch")
     T, K = idx.shape
-    st = _launch_stream(stream, *[t.get_device() for t in (offsets, perm, inv, idx, ws)])
+    st = _launch_stream(stream, *devices)
     _check("k3g_moe_sort", lib().k3g_moe_sort(offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), idx.data_ptr(), T, K,
                                               offsets.numel() - 1, ws.data_ptr(), ws.numel(), st))
     return offsets, perm, inv
@@ -697,17 +708,15 @@ def k3g_moe_sort(offsets: torch.Tensor, perm: torch.Tensor, inv: torch.Tensor, i
 
 def _pairs(tok, rows, inv, wts, dwts, stream, *others):
     """What the calls on pairs' rows check alike; returns (T, K, rows, columns, stream)."""
-    _dev(inv, torch.int32, "inv")
+    devices = [_flat(inv, torch.int32, "inv"), tok.get_device(), rows.get_device()]
     if inv.dim() != 2:
         raise ValueError("inv must be [T, K]")
     T, K = inv.shape
-    devices = [inv.get_device(), tok.get_device(), rows.get_device()]
     for name, t in (("wts", wts), ("dwts", dwts)):
         if t is not None:
-            _dev(t, torch.float32, name)
+            devices.append(_flat(t, torch.float32, name))
             if t.shape != inv.shape:
                 raise ValueError(f"{name} must be [T, K]")
-            devices.append(t.get_device())
     devices += [t.get_device() for t in others if t is not None]
     return T, K, rows.shape[0], rows.shape[1], _launch_stream(stream, *devices)
 
@@ -845,15 +854,13 @@ def _int4_groups(y, x, w: Int4, offsets, perm, top_k: int, stream):
     """What the grouped calls check alike; returns (y's row stride, x's, the stream)."""
     xld = _rows(x, "x", -1, w.n_in)
     ld = _rows(y, "the output", -1, w.rows)
-    _dev(offsets, torch.int32, "offsets")
+    devices = [y.get_device(), x.get_device(), w.device, _flat(offsets, torch.int32, "offsets")]
     if offsets.numel() != w.n_experts + 1:
         raise ValueError("offsets must have n_experts + 1 entries")
-    devices = [y.get_device(), x.get_device(), w.device, offsets.get_device()]
     if perm is not None:
-        _dev(perm, torch.int32, "perm")
+        devices.append(_flat(perm, torch.int32, "perm"))
         if perm.numel() != y.shape[0]:
             raise ValueError("perm must have an entry a row")
-        devices.append(perm.get_device())
     elif x.shape[0] < y.shape[0]:
         raise ValueError("without perm, x must have a row for each row of the output")
     if top_k < 1:

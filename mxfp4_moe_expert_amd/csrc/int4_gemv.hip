@@ -60,21 +60,6 @@ __device__ inline float dot32(const uint4 &w, const float *x) {
     return s0 + s1;
 }
 
-// The wavefront's sums of four values, value i in the lanes l with l % 4 = i: two
-// exchanges within a quad halve what is left each time, then quads and rows are added.
-__device__ inline float wave_sum4(const float *y, int lane) {
-    const bool odd = lane & 1, up = lane & 2;
-    const float a = (odd ? y[1] : y[0]) + dpp<0xB1>(odd ? y[0] : y[1]);
-    const float b = (odd ? y[3] : y[2]) + dpp<0xB1>(odd ? y[2] : y[3]);
-    float v = (up ? b : a) + dpp<0x4E>(up ? a : b);
-    v += dpp<0x124>(v);  // row_ror:4
-    v += dpp<0x128>(v);  // row_ror:8
-    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    v = __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
-    const auto t = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    return __builtin_bit_cast(float, (uint32_t)t[0]) + __builtin_bit_cast(float, (uint32_t)t[1]);
-}
-
 // NW weights (2: the gated up-product), CH loads of 2048 columns a wavefront, S32: fp32 scales.
 template <int NW, int CH, bool S32>
 __global__ __launch_bounds__(kGvWaves * kWave) void int4_gemv_kernel(GvArgs g) {

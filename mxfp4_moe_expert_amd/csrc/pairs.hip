@@ -102,20 +102,28 @@ __global__ __launch_bounds__(NT) void sort_kernel(int32_t *__restrict__ offsets,
         }
         if (write && tid == 0) offsets[E] = kept;
     };
-    if (counts) {
-        for (int e = tid; e < E; e += NT) {
+    if (counts) {  // an expert's pairs in all chunks, and in those before this one (two experts a thread at most)
+        static_assert(NT < 1024 || kSortMaxExperts <= 2 * NT, "");
+        int before[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = tid + k * NT;
+            if (e >= E) continue;
             int all = 0;
-            for (int c = 0; c < (int)gridDim.x; ++c) all += counts[(int64_t)c * E + e];
+#pragma unroll 16
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int n = counts[(int64_t)c * E + e];
+                all += n;
+                before[k] += c < (int)blockIdx.x ? n : 0;
+            }
             sum[e] = all;
         }
         __syncthreads();
         place(blockIdx.x == 0);
         __syncthreads();
-        for (int e = tid; e < E; e += NT) {  // what the chunks before this one hold
-            int before = 0;
-            for (int c = 0; c < (int)blockIdx.x; ++c) before += counts[(int64_t)c * E + e];
-            next[e] += before;
-        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (tid + k * NT < E) next[tid + k * NT] += before[k];
     }
     int bits = 1;
     while ((1 << bits) < E) ++bits;
@@ -213,24 +221,48 @@ struct PairArgs {
 
 constexpr int kPairCols = 8;  // columns of a thread
 
-// The columns of a row that are there: eight, or the first of them.
-template <int TYPE>
+typedef uint32_t Bits __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any entry's address
+
+// The columns of a row that are there: eight, or the first of them. ONCE: past the caches.
+template <int TYPE, bool ONCE>
 __device__ inline void load_cols(float *v, const void *base, int64_t at, int n) {
     typedef typename Elem<TYPE>::T T;
     const T *p = (const T *)base + at;
     if (n >= kPairCols) {
-        load_n<TYPE, kPairCols>(v, p);
+        if constexpr (ONCE) {
+            constexpr int M = kPairCols * sizeof(T) / 16;
+            Bits b[M];
+            T t[kPairCols];
+#pragma unroll
+            for (int i = 0; i < M; ++i) b[i] = __builtin_nontemporal_load((const Bits *)p + i);
+            __builtin_memcpy(t, b, sizeof t);
+#pragma unroll
+            for (int i = 0; i < kPairCols; ++i) v[i] = Elem<TYPE>::load(t[i]);
+        } else {
+            load_n<TYPE, kPairCols>(v, p);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kPairCols; ++i) v[i] = i < n ? Elem<TYPE>::load(p[i]) : 0.0f;
     }
 }
-template <int TYPE>
+template <int TYPE, bool ONCE>
 __device__ inline void store_cols(void *base, int64_t at, int n, const float *v) {
     typedef typename Elem<TYPE>::T T;
     T *p = (T *)base + at;
     if (n >= kPairCols) {
-        store_n<TYPE, kPairCols>(p, v);
+        if constexpr (ONCE) {
+            constexpr int M = kPairCols * sizeof(T) / 16;
+            Bits b[M];
+            T t[kPairCols];
+#pragma unroll
+            for (int i = 0; i < kPairCols; ++i) t[i] = Elem<TYPE>::store(v[i]);
+            __builtin_memcpy(b, t, sizeof t);
+#pragma unroll
+            for (int i = 0; i < M; ++i) __builtin_nontemporal_store(b[i], (Bits *)p + i);
+        } else {
+            store_n<TYPE, kPairCols>(p, v);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kPairCols; ++i)
@@ -241,8 +273,9 @@ __device__ inline void store_cols(void *base, int64_t at, int n, const float *v)
 // SCATTER: sorted rows are written from the token's row. SUM: the sorted rows are
 // summed into the token's. DOT: their products with the token's row are summed.
 // An item: a token, a part of its columns and (no SUM) some of its pairs; DOT
-// takes all columns. U sorted rows are loaded at a time.
-template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT, int U>
+// takes all columns. Lane k holds the sorted row and the weight of pair k of the item;
+// U sorted rows are loaded at a time.
+template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT, int U, bool ONCE>
 __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
     __shared__ float part[DOT ? 16 * kPairMaxTopK : 1];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -251,55 +284,72 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t t = item / (turns * a.parts);
         const int rest = (int)(item - t * (turns * a.parts)), turn = rest / a.parts;
-        const int k0 = turn * a.slots, k1 = min(k0 + a.slots, a.K);
-        const int32_t *inv = a.inv + t * a.K;
-        if (DOT)
-            for (int k = lane; k < k1 - k0; k += kWave) part[wave * kPairMaxTopK + k] = 0.0f;
+        const int k0 = turn * a.slots, n_pairs = min(a.slots, a.K - k0);
+        int mine = lane < n_pairs ? a.inv[t * a.K + k0 + lane] : -1;
+        if ((unsigned)mine >= (unsigned)a.R) mine = -1;
+        const float weight = mine < 0 ? 0.0f : a.wts ? a.wts[t * a.K + k0 + lane] : 1.0f;
+        if (DOT) part[wave * kPairMaxTopK + lane] = 0.0f;
         for (int c0 = (rest - turn * a.parts) * width; c0 < a.n; c0 += a.parts * width) {
             const int c = c0 + tid * kPairCols, n = a.n - c;
             float tok[kPairCols], sum[kPairCols] = {};
-            if (SCATTER || DOT) load_cols<TOK>(tok, a.tok, n > 0 ? t * a.tok_ld + c : 0, n);
-            for (int k = k0; k < k1; k += U) {
-                int p[U];
+            if (SCATTER || DOT) load_cols<TOK, false>(tok, a.tok, n > 0 ? t * a.tok_ld + c : 0, n);
+            for (int k = 0; k < n_pairs; k += U) {
+                int p[U], common = -1, some = 0;
                 float w[U], v[U][kPairCols];
 #pragma unroll
                 for (int j = 0; j < U; ++j) {
-                    p[j] = k + j < k1 ? inv[k + j] : -1;
-                    if ((unsigned)p[j] >= (unsigned)a.R) p[j] = -1;
-                    if (SCATTER || SUM) w[j] = a.wts && p[j] >= 0 ? a.wts[t * a.K + k + j] : 1.0f;
+                    p[j] = __builtin_amdgcn_readlane(mine, k + j);
+                    w[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), k + j));
+                    common &= p[j];
+                    some |= p[j];
                 }
+                if (common < 0) continue;  // none has a row
                 if (SUM || DOT) {
 #pragma unroll
-                    for (int j = 0; j < U; ++j)
-                        if (p[j] >= 0) load_cols<ROW>(v[j], a.row, n > 0 ? p[j] * a.row_ld + c : 0, n);
-                }
+                    for (int j = 0; j < U; ++j) load_cols<ROW, ONCE>(v[j], a.row, n > 0 ? max(p[j], 0) * a.row_ld + c : 0, n);
+                    if (some < 0) {  // a pair without a row adds nothing, whatever the row read in its place holds
 #pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    if (p[j] < 0) continue;
-                    if (SUM) {
+                        for (int j = 0; j < U; ++j)
+#pragma unroll
+                            for (int i = 0; i < kPairCols; ++i) v[j][i] = p[j] < 0 ? 0.0f : v[j][i];
+                    }
+                }
+                if (SUM) {
+#pragma unroll
+                    for (int j = 0; j < U; ++j)
 #pragma unroll
                         for (int i = 0; i < kPairCols; ++i) sum[i] = __builtin_fmaf(w[j], v[j][i], sum[i]);
-                    }
-                    if (DOT) {
-                        float d = 0.0f;
+                }
+                if (DOT) {
 #pragma unroll
-                        for (int i = 0; i < kPairCols; ++i) d = __builtin_fmaf(tok[i], v[j][i], d);
-                        d = wave_sum(d);
-                        if (lane == 0) part[wave * kPairMaxTopK + k + j - k0] += d;
+                    for (int j = 0; j < U; j += 4) {
+                        float d[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            d[m] = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < kPairCols; ++i) d[m] = __builtin_fmaf(tok[i], v[j + m][i], d[m]);
+                        }
+                        const float all4 = wave_sum4(d, lane);
+                        if (lane < 4) part[wave * kPairMaxTopK + k + j + lane] += all4;
                     }
-                    if (SCATTER) {
+                }
+                if (SCATTER) {
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        if (p[j] < 0) continue;
                         float u[kPairCols];
 #pragma unroll
                         for (int i = 0; i < kPairCols; ++i) u[i] = w[j] * tok[i];
-                        store_cols<ROW>(a.row_out, n > 0 ? p[j] * a.row_out_ld + c : 0, n, u);
+                        store_cols<ROW, ONCE>(a.row_out, n > 0 ? p[j] * a.row_out_ld + c : 0, n, u);
                     }
                 }
             }
-            if (SUM) store_cols<TOK>(a.tok_out, n > 0 ? t * a.tok_out_ld + c : 0, n, sum);
+            if (SUM) store_cols<TOK, false>(a.tok_out, n > 0 ? t * a.tok_out_ld + c : 0, n, sum);
         }
         if (DOT) {
             __syncthreads();
-            for (int k = tid; k < k1 - k0; k += a.waves * kWave) {
+            for (int k = tid; k < n_pairs; k += a.waves * kWave) {
                 float d = part[k];
                 for (int w = 1; w < a.waves; ++w) d += part[w * kPairMaxTopK + k];
                 a.dwts[t * a.K + k0 + k] = d;
@@ -308,6 +358,8 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
         }
     }
 }
+
+constexpr int64_t kPairFew = 4096;  // wavefronts below which items are made smaller
 
 template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT>
 int launch_pairs(PairArgs a, hipStream_t st) {
@@ -320,16 +372,20 @@ int launch_pairs(PairArgs a, hipStream_t st) {
         a.waves = row_waves < 8 ? row_waves : 8;
         a.parts = (row_waves + a.waves - 1) / a.waves;
     }
-    if (SUM && !DOT && (int64_t)a.T * a.parts * a.waves < 4096) {  // few tokens: all of their rows at once
-        a.parts = row_waves;
-        a.waves = 1;
-        const int64_t items = (int64_t)a.T * a.parts;
-        pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, 16><<<(unsigned)items, kWave, 0, st>>>(a);
-        return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
+    const bool few = (int64_t)a.T * a.parts * a.waves < kPairFew;
+    if (few) {
+        if (!SUM) a.slots = a.K < 4 ? a.K : 4;
+        if (!DOT) {
+            a.parts = row_waves;
+            a.waves = 1;
+        }
     }
     const int64_t items = (int64_t)a.T * a.parts * ((a.K + a.slots - 1) / a.slots), most = 1 << 20;
-    pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, 4>
-        <<<(unsigned)(items < most ? items : most), a.waves * kWave, 0, st>>>(a);
+    const unsigned grid = (unsigned)(items < most ? items : most), threads = a.waves * kWave;
+    if (!few)
+        pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, 4, true><<<grid, threads, 0, st>>>(a);
+    else  // (a sum alone: all of a token's rows at once)
+        pairs_kernel<ROW, TOK, SCATTER, SUM, DOT, SUM && !DOT ? 16 : 4, false><<<grid, threads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
