@@ -551,7 +551,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
  *   packed [n_experts][rows][in/2]: codes n of 0 .. 15, two per byte, the LOW nibble
  *          is the even column;
  *   scales [n_experts][rows][in/group] of scale_type (a k3g_type);
- *   zeros  uint8 [n_experts][rows][in/group], or null: all 8;
+ *   zeros  uint8 [n_experts][rows][in/group], each at most 128, or null: all 8;
  * an element is (n - zero) * scale of its group. group 32, 64 or 128; in a positive
  * multiple of group, at most 65536; rows <= 2^30, n_experts <= 2048
  * (K3G_EUNSUPPORTED beyond). packed 16-byte aligned, scales to their type. */
@@ -692,6 +692,12 @@ int k3g_probe_handoff(int mode, int n_wg, float *buf, uint32_t *counter, void *s
  * together). rows: outputs. Tiles of up to 32 outputs are the streaming kernel's.
  * K3G_EINVAL for a size that the call refuses. */
 int k3g_probe_mx_form(int a_format, int kind, int n_rows, int rows, int n_experts);
+
+/* k3g_probe_int4_form: the same for int4 products of x_type activations (aligned: x and
+ * its row stride on 16-byte addresses): weight rows << 16 | tokens of the tile, for
+ * kind 0 k3g_int4_matmul, 1 k3g_int4_grouped_matmul, 2 k3g_int4_grouped_glu. One token: the
+ * vector kernel's; up to 64 weight rows: the streaming kernels'. */
+int k3g_probe_int4_form(int x_type, int aligned, int kind, int n_rows, int rows, int in, int n_experts);
 
 #ifdef __cplusplus
 }

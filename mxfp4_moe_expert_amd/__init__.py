@@ -157,6 +157,7 @@ def lib():
         L.k3g_probe_read_rate.argtypes = [P, sz, P, P]
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
         L.k3g_probe_mx_form.argtypes = [i, i, i, i, i]
+        L.k3g_probe_int4_form.argtypes = [i, i, i, i, i, i, i]
         _lib = L
     return _lib
 
@@ -928,6 +929,17 @@ def k3g_probe_mx_form(a_format: int, n_rows: int, rows: int, n_experts: int = 0,
     f = lib().k3g_probe_mx_form(a_format, 2 if glu else 1 if n_experts else 0, n_rows, rows, n_experts)
     if f < 0:
         _check("k3g_probe_mx_form", f)
+    return f >> 16, f & 0xFFFF
+
+
+def k3g_probe_int4_form(x_type: torch.dtype, n_rows: int, rows: int, n_in: int, n_experts: int = 0, glu: bool = False,
+                        aligned: bool = True) -> tuple[int, int]:
+    """(weight rows, tokens) of the tile that an int4 product of these sizes runs on: dense, or of experts. One token:
+    the vector kernel; up to 64 weight rows: the streaming kernels."""
+    f = lib().k3g_probe_int4_form(_TYPES[x_type], int(aligned), 2 if glu else 1 if n_experts else 0, n_rows, rows, n_in,
+                                  n_experts)
+    if f < 0:
+        _check("k3g_probe_int4_form", f)
     return f >> 16, f & 0xFFFF
 
 

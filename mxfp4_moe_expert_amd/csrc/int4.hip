@@ -140,4 +140,13 @@ int k3g_int4_grouped_glu(void *h, int h_type, int64_t h_stride, const void *x, i
     return launch(a, GLU, x_type, w1->group, stream);
 }
 
+int k3g_probe_int4_form(int x_type, int aligned, int kind, int n_rows, int rows, int in, int n_experts) {
+    if (!type_ok(x_type) || kind < DENSE || kind > GLU || n_rows < 1 || rows < 1 || in < 32 || in % 32 || in > kMxMaxIn ||
+        n_rows > kMaxRows || rows > kMaxRows || (kind != DENSE && (n_experts < 1 || n_experts > kMaxExperts)))
+        return K3G_EINVAL;
+    I4Args a = {};
+    a.T = n_rows, a.rows = rows, a.in = in, a.E = n_experts, a.x_vec = aligned != 0;
+    return product_form(a, kind, x_type);
+}
+
 }  // extern "C"

@@ -10,14 +10,21 @@
 //   gather_backward   dx[t] = sum_k w[t][k] dys[inv[t][k]],  dw[t][k] = <x[t], dys[inv[t][k]]>
 //   combine_backward  dys[inv[t][k]] = w[t][k] dy[t],        dw[t][k] = <dy[t], ys[inv[t][k]]>
 // One kernel does all four, token by token: each sorted row belongs to one pair,
-// so nothing is added by two workgroups and results do not depend on timing.
+// so nothing is added by two workgroups and results do not depend on timing. HBM
+// bounds it at a prompt's size: of 4096 x 16 rows of 3584 bf16, written 84 us (5.4 TB/s),
+// summed into fp32 100 us (5.3), summed with the dot products 110 us (4.4), written with the
+// dot products 194 us (5.2; 1 GB). Sorted rows are read and written once and are
+// more than the caches hold, so they pass them by (written through them 145 us,
+// read through them 109 and 114). A batch of 64 tokens takes 5 to 9 us: a launch, and loads
+// that wait for each other.
 #include "mx.h"
 
 namespace k3g {
 
 constexpr int kSortMaxExperts = 2048;
 constexpr int kPairMaxTopK = 64;
-constexpr int kSortChunk = 4096;     // pairs that a workgroup ranks at a time
+constexpr int kSortAlone = 4096;     // pairs that one workgroup sorts in one launch
+constexpr int kSortChunk = 2048;     // pairs that a workgroup of several ranks at a time
 constexpr int kSortMaxChunks = 256;  // workgroups of a large sort
 
 // ---- sort ------------------------------------------------------------------------
@@ -30,11 +37,16 @@ constexpr int kSortMaxChunks = 256;  // workgroups of a large sort
 // wavefronts is added when all have counted. One workgroup does up to 4096 pairs
 // in one launch; more are cut into chunks, whose histograms a first launch
 // writes and whose starts each workgroup of the second sums up itself.
+//
+// Latency bounds it: the bytes of 131,056 pairs would take under 1 us. In us, 896
+// experts: 1,024 pairs 5.0 (the kernel alone), 4,096 8.7 (by two launches 9.9), 131,056
+// 13.3 (chunks of 1,024 14.8, of 4,096 14.3), 960,000 30.
 
 // The chunks of P pairs, and the pairs of each (a multiple of kSortChunk).
 int sort_chunks(int64_t P) {
+    if (P <= kSortAlone) return 1;
     const int64_t n = (P + kSortChunk - 1) / kSortChunk;
-    return n < 1 ? 1 : n < kSortMaxChunks ? (int)n : kSortMaxChunks;
+    return n < kSortMaxChunks ? (int)n : kSortMaxChunks;
 }
 inline int64_t sort_chunk_pairs(int64_t P) {
     const int n = sort_chunks(P);
@@ -359,7 +371,9 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
     }
 }
 
-constexpr int64_t kPairFew = 4096;  // wavefronts below which items are made smaller
+// Wavefronts below which items are made smaller: columns, or slots, in workgroups of their own (61 tokens: rows
+// written 9.4 us, so 5.6; summed 8.0, 6.2; written with the dot products, 64 tokens of fp32, 16.5, 9.2).
+constexpr int64_t kPairFew = 4096;
 
 template <int ROW, int TOK, bool SCATTER, bool SUM, bool DOT>
 int launch_pairs(PairArgs a, hipStream_t st) {
@@ -478,7 +492,7 @@ int k3g_moe_sort(int32_t *offsets, int32_t *perm, int32_t *inv, const int32_t *i
     if (chunks == 1) {
         if (P <= 256) return launch_sort<256, 1>(offsets, perm, inv, idx, nullptr, (int)P, E, 1, 256, st);
         if (P <= 1024) return launch_sort<1024, 1>(offsets, perm, inv, idx, nullptr, (int)P, E, 1, 1024, st);
-        return launch_sort<1024, 4>(offsets, perm, inv, idx, nullptr, (int)P, E, 1, kSortChunk, st);
+        return launch_sort<1024, 4>(offsets, perm, inv, idx, nullptr, (int)P, E, 1, kSortAlone, st);
     }
     k3g_ws_layout l;
     K3G_TRY(k3g_workspace_layout(&l, K3G_OP_MOE_SORT, &shape));
@@ -486,7 +500,7 @@ int k3g_moe_sort(int32_t *offsets, int32_t *perm, int32_t *inv, const int32_t *i
     const int per = (int)sort_chunk_pairs(P);
     sort_count_kernel<<<chunks, 1024, 0, st>>>(counts, idx, (int)P, E, per);
     if (hipGetLastError() != hipSuccess) return K3G_EHIP;
-    return launch_sort<1024, 4>(offsets, perm, inv, idx, counts, (int)P, E, chunks, per, st);
+    return launch_sort<1024, 2>(offsets, perm, inv, idx, counts, (int)P, E, chunks, per, st);
 }
 
 int k3g_moe_gather(void *ys, int ys_type, int64_t ys_stride, const void *x, int x_type, int64_t x_stride,

@@ -36,7 +36,9 @@ def untouched(b, T, rows):
 DENSE = [(1, 32, 1, 32), (1, 64, 17, 64), (1, 128, 16, 128), (2, 96, 33, 32), (1, 7168, 3584, 64), (3, 320, 100, 64),
          (15, 544, 31, 32), (16, 640, 64, 128), (17, 1056, 48, 32), (31, 4224, 40, 128), (33, 3584, 129, 64),
          (61, 3584, 7168, 32), (64, 4160, 257, 32), (65, 512, 130, 128), (127, 1120, 77, 32), (200, 2048, 300, 64),
-         (4, 65536, 5, 32), (1000, 256, 512, 64), (300, 768, 4097, 128)]
+         (4, 65536, 5, 32), (1000, 256, 512, 64), (300, 768, 4097, 128), (1, 34816, 40, 64),
+         # tiles: ragged outputs and tokens, an odd number of 32-column blocks, ends inside a turn of 256 columns
+         (300, 352, 9701, 32), (515, 704, 5900, 64), (500, 640, 11000, 128), (385, 32, 9700, 32)]
 
 
 @pytest.mark.parametrize("xt", TYPES, ids=name)
@@ -129,6 +131,41 @@ def test_not_finite(k3g):
             assert torch.equal(y[~hit][:, rows], good[~hit][:, rows]) and not torch.isfinite(y[:, ~rows]).any()
 
 
+def test_zeros_at_both_ends_and_tensors_off_their_alignment(k3g):
+    """Zeros of 0, 15 and 128; scales and zeros that begin at any entry, next to marked ones."""
+    for T, n, rows in ((1, 320, 50), (7, 320, 50), (40, 320, 50), (515, 320, 5900)):
+        for xt in TYPES:
+            g = gen(T)
+            packed, s, _ = ref.random_weights(g, (rows,), n, 32, torch.bfloat16, False, exact=True)
+            z = torch.tensor([0, 15, 128], dtype=torch.uint8, device="cuda")[torch.randint(0, 3, s.shape, device="cuda", generator=g)]
+            sb = torch.full((s.numel() + 9,), float("nan"), dtype=s.dtype, device="cuda")
+            zb = torch.full((z.numel() + 9,), 77, dtype=torch.uint8, device="cuda")
+            s1, z1 = sb[3:3 + s.numel()].view(s.shape), zb[5:5 + z.numel()].view(z.shape)
+            s1.copy_(s), z1.copy_(z)
+            x = ref.rows_of(g, T, n, xt, exact=True).contiguous()
+            y = torch.empty(T, rows, device="cuda")
+            k3g.k3g_int4_matmul(y, x, k3g.int4(packed, s1, z1))
+            assert torch.equal(y.double(), x.double() @ ref.values(packed, s, z)[0].t().contiguous()), (T, xt)
+
+
+def test_the_sizes_above_reach_every_kernel(k3g):
+    """The tiles (weight rows, tokens) that the tests' sizes run on, by kind and type of x."""
+    form = k3g.k3g_probe_int4_form
+    for xt in TYPES:
+        wide = (256, 64) if xt == torch.float32 else (256, 128)
+        dense = {form(xt, T, rows, n) for T, n, rows, _ in DENSE}
+        assert dense == {(8, 1), (16, 16), (32, 16), (64, 32), wide}
+        if xt != torch.float32:
+            assert (256, 64) in {form(xt, T, rows, n, aligned=False) for T, n, rows, _ in DENSE}
+        for glu in (False, True):
+            assert {form(xt, R, rows, n, E, glu) for E, R, n, rows, _, _ in GROUPED} == {(8, 1), (32, 16), (64, 32), wide}
+            assert (256, 64) in {form(xt, R, rows, n, E, glu, aligned=False) for E, R, n, rows, _, _ in GROUPED}
+        for group in (32, 64, 128):  # every group on tiles, dense and grouped
+            assert any(form(xt, T, rows, n) == wide for T, n, rows, g in DENSE if g == group)
+            for glu in (False, True):
+                assert any(form(xt, R, rows, n, E, glu) == wide for E, R, n, rows, g, _ in GROUPED if g == group)
+
+
 def test_no_tokens(k3g):
     w = ref.random_weights(gen(0), (8,), 64, 32, torch.float32, False)
     k3g.k3g_int4_matmul(torch.empty(0, 8, device="cuda"), torch.empty(0, 64, device="cuda"), k3g.int4(*w))
@@ -147,7 +184,11 @@ def ragged(g, E, n_rows, before=0, behind=0):
 
 # (experts, rows, columns, outputs, group, top_k): few and many rows an expert, one expert, more experts than rows
 GROUPED = [(1, 5, 64, 16, 32, 1), (7, 40, 128, 48, 64, 2), (896, 64, 96, 33, 32, 16), (30, 700, 640, 100, 128, 4),
-           (5, 400, 544, 257, 32, 3), (64, 1000, 1536, 128, 64, 8), (3, 1500, 256, 384, 128, 1), (2048, 300, 64, 8, 32, 6)]
+           (5, 400, 544, 257, 32, 3), (64, 1000, 1536, 128, 64, 8), (3, 1500, 256, 384, 128, 1), (2048, 300, 64, 8, 32, 6),
+           # tiles
+           (16, 1500, 352, 2000, 32, 1), (12, 1400, 448, 2600, 64, 4), (13, 1300, 640, 2401, 128, 2),
+           # the vector kernel: rows of experts, more rows than an expert's share
+           (896, 16, 3584, 100, 32, 16), (200, 64, 2112, 33, 64, 1), (130, 60, 6272, 70, 128, 7)]
 
 
 @pytest.mark.parametrize("xt", TYPES, ids=name)
@@ -161,6 +202,8 @@ def test_grouped(k3g, E, R, n, rows, group, k, xt):
         perm = torch.randperm(R, generator=g, device="cuda").int()
         x = ref.rows_of(g, (R + k - 1) // k, n, xt, pad=1)
         straight = ref.rows_of(g, R, n, xt)
+        if zeros:  # on 16-byte addresses, the other time off them
+            x, straight = x.contiguous(), straight.clone()
         for source, p in ((x, perm), (straight, None)):
             b, y = output(R, rows, yt, pad=2)
             k3g.k3g_int4_grouped_matmul(y, source, k3g.int4(*w), off, perm=p, top_k=k)
@@ -189,6 +232,7 @@ def test_glu(k3g, E, R, n, rows, group, k, xt):
         off = ragged(g, E, R)
         perm = torch.randperm(R, generator=g, device="cuda").int()
         x = ref.rows_of(g, (R + k - 1) // k, n, xt)
+        x = x.clone() if zeros else x
         b, h = output(R, rows, ht)
         k3g.k3g_int4_grouped_glu(h, x, k3g.int4(*w1), k3g.int4(*w3), off, perm=perm, top_k=k)
         a = x.double()[perm.long() // k]

@@ -78,3 +78,21 @@ def test_binding_refuses(k3g):
               lambda: k3g.int4(p.int(), s), lambda: k3g.int4(p, s.double())):
         with pytest.raises((ValueError, TypeError)):
             f()
+
+
+def test_form(k3g):
+    """Which kernel a product runs on, and the refusals of the question."""
+    import torch
+    f32, b16, form = torch.float32, torch.bfloat16, k3g.k3g_probe_int4_form
+    assert form(b16, 1, 3584, 7168) == (8, 1) and form(b16, 1, 8, 65536) == (16, 16)
+    assert form(b16, 16, 3584, 7168) == (16, 16) and form(b16, 16, 7168, 3584) == (32, 16)
+    assert form(b16, 33, 3584, 7168) == (64, 32) and form(b16, 1024, 3584, 7168) == (256, 128)
+    assert form(b16, 1024, 3584, 7168, aligned=False) == (256, 64) and form(f32, 1024, 3584, 7168) == (256, 64)
+    assert form(f32, 512, 3584, 7168) == (64, 32)
+    assert form(f32, 16, 3072, 3584, 896, glu=True) == (8, 1) and form(b16, 1024, 3072, 3584, 896, glu=True) == (32, 16)
+    assert form(b16, 16 * 896, 3584, 3072, 896) == (64, 32) and form(b16, 65536, 3584, 3072, 896) == (256, 128)
+    L = k3g.lib()
+    ok = [1, 1, 1, 64, 64, 64, 8]
+    assert L.k3g_probe_int4_form(*ok) > 0
+    for i, bad in ((0, 3), (2, 3), (2, -1), (3, 0), (4, 0), (5, 0), (5, 48), (5, 1 << 17), (6, 0), (6, 2049)):
+        assert L.k3g_probe_int4_form(*[bad if j == i else v for j, v in enumerate(ok)]) == EINVAL, (i, bad)

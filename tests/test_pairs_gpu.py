@@ -128,7 +128,7 @@ def maps(inv, R):
 
 SHAPES = [(1, 1, 1, 1, 0), (1, 16, 16, 7168, 0), (5, 3, 9, 63, 5), (33, 4, 140, 512, 1), (7, 64, 448, 520, 0),
           (64, 16, 1024, 3584, 8), (61, 9, 300, 3585, 3), (3, 5, 15, 65536, 0), (9, 2, 0, 40, 0), (2, 7, 14, 8200, 2),
-          (1500, 6, 9000, 96, 0)]
+          (1500, 6, 9000, 96, 0), (4200, 3, 13000, 96, 1), (701, 5, 3000, 3003, 3)]
 PAIRS = [(a, b) for a in TYPES for b in TYPES]
 
 
