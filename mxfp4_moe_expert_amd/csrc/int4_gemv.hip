@@ -29,9 +29,12 @@ struct GvArgs {
 __device__ inline int expert_of(const I4Args &a, int p) {
     const int lane = threadIdx.x & (kWave - 1);
     int e = 0;
-    for (int i = 0; i < a.E; i += kWave) {
-        const bool before = i + lane < a.E && a.offsets[i + lane + 1] <= p;
-        e += __popcll(__ballot(before));
+    for (int i = 0; i < a.E; i += 8 * kWave) {  // eight loads under way at once
+        int ends[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ends[k] = a.offsets[min(i + k * kWave + lane, a.E - 1) + 1];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e += __popcll(__ballot(i + k * kWave + lane < a.E && ends[k] <= p));
     }
     e = __builtin_amdgcn_readfirstlane(e);
     return e < a.E && a.offsets[e] <= p && p < a.offsets[e + 1] ? e : -1;
