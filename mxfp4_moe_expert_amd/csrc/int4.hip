@@ -32,23 +32,27 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 // each (us; vector, streamed): one bf16 token 7168 -> 3584 8.6, 9.4; two 9.7, 9.5 (fp32 3584 -> 7168 8.8, 13.5; 11.1,
 // 13.6); 64 rows of 256 experts 88, 135; 256 rows 290, 250.
 //
-// Tiles of 256 outputs pay where rows are many and items enough to fill half of the chip: 3584 -> 7168 of bf16, 512
-// tokens (112 items) streamed 93, tiled 100, 1024 tokens 182, 102; 7168 -> 3584, 1024 tokens (112) 156, 185, 1536 227, 184.
+// Tiles of 256 outputs pay where rows are many and items enough to fill half of the chip (streamed, tiled): bf16 3584
+// -> 7168, 512 tokens (112 items) 100, 100, 1024 tokens (224) 182, 102; 7168 -> 3584, 1024 tokens (112) 138, 185, 1536
+// (168) 207, 184.
 // fp32 (64 tokens a tile) 7168 -> 3584, 512 tokens (112) 144, 219, 1024 (224) 253, 222. Grouped, by the average rows of the
 // bank's experts: 256 of 3584 x 3584, bf16, 16 rows 584, 623, 32 rows 873, 698; fp32 64 rows 635, 684, 128 rows 1133, 1025.
 //
 // Streamed, 64 outputs by 32 tokens, or 32 by 16 where that leaves half a tile empty: 7168 -> 3584, 32 tokens (32 x
 // 16 first) 14, 27, 64 tokens 22, 26, 96 30, 26 (3584 -> 7168: 19, 20; 34, 20); grouped 256 x 4 rows 467, 525, 16 rows 725,
-// 584. Up to 16 tokens of few outputs take 16 a workgroup: 7168 -> 3584, 16 tokens 11, 14; 3584 -> 7168 12, 11.
+// 584. Up to 16 tokens of few outputs take 16 a workgroup: 7168 -> 3584, 16 tokens 11, 14; 3584 -> 7168 12, 11. Where
+// 64 x 32 would be more than a workgroup a CU, bf16 and fp16 take 64 x 64: 7168 -> 3584, 128 tokens (224) 25, 39, 192 47,
+// 38, 512 91, 71; 3584 -> 7168, 64 tokens (224) 20, 29, 128 36, 29 (fp32 49, 55; 512 tokens 162, 206).
 int product_form(const I4Args &a, int mode, int x_type) {
     if (a.in <= kGvMaxIn && (a.T == 1 || (mode != DENSE && a.T <= 64 && 2 * a.T <= a.E))) return form(8, 1);
     const bool wide = x_type != K3G_F32 && a.x_vec;
     const int64_t n = mode == DENSE ? a.T : ((int64_t)a.T + a.E - 1) / a.E, most = wide ? 128 : 64;
     const int64_t tiles = mode == DENSE ? (n + most - 1) / most : (n + most - 1) / most * (a.E < a.T ? a.E : a.T);
     const int64_t items = ((int64_t)a.rows + 255) / 256 * tiles * (mode == GLU ? 2 : 1);
-    if (n > (wide ? 20 : 80) && items >= (wide ? 112 : 160)) return wide ? form(256, 128) : form(256, 64);
+    if (n > (wide ? 20 : 80) && items >= (wide ? 128 : 160)) return wide ? form(256, 128) : form(256, 64);
     if (mode == DENSE && a.T <= 16 && a.rows <= 16 * 256) return form(16, 16);
-    return n <= (mode == DENSE ? 32 : 8) ? form(32, 16) : form(64, 32);
+    if (n <= (mode == DENSE ? 32 : 8)) return form(32, 16);
+    return mode == DENSE && x_type != K3G_F32 && (a.rows + 63) / 64 * ((n + 31) / 32) > 256 ? form(64, 64) : form(64, 32);
 }
 
 int launch(I4Args &a, int mode, int x_type, int group, void *stream) {

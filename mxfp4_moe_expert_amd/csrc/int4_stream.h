@@ -191,6 +191,8 @@ int launch_int4_stream_form(const I4Args &a, int f, hipStream_t st) {
     if constexpr (MODE == DENSE)
         if (f == form(16, 16)) return launch_int4_stream<XT, GROUP, MODE, 1, 1>(a, st);
     if (f == form(32, 16)) return launch_int4_stream<XT, GROUP, MODE, 2 / NW, 1>(a, st);
+    if constexpr (MODE == DENSE && XT != K3G_F32)
+        if (f == form(64, 64)) return launch_int4_stream<XT, GROUP, MODE, 4, 4>(a, st);
     return launch_int4_stream<XT, GROUP, MODE, 4 / NW, 2>(a, st);
 }
 
