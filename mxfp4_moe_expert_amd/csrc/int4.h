@@ -136,6 +136,47 @@ __device__ inline void scales_at(float *v, const void *s, int type, int64_t i) {
         load_n<K3G_F16, N>(v, (const _Float16 *)s + i);
 }
 
+typedef const __attribute__((address_space(1))) uint8_t *global_t;
+
+// BYTES (2, 4, 8 or 16) from any address into whole registers.
+template <int BYTES>
+__device__ inline void load_raw(uint32_t *v, global_t p) {
+    if constexpr (BYTES == 2) {
+        typedef uint16_t U __attribute__((aligned(1)));
+        v[0] = *(const __attribute__((address_space(1))) U *)p;
+    } else if constexpr (BYTES == 4) {
+        typedef uint32_t U __attribute__((aligned(1)));
+        v[0] = *(const __attribute__((address_space(1))) U *)p;
+    } else {
+        typedef uint32_t U __attribute__((ext_vector_type(BYTES / 4), aligned(1)));
+        const U u = *(const __attribute__((address_space(1))) U *)p;
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) v[i] = u[i];
+    }
+}
+
+// The scales and zeros of N (2, 4 or 8) consecutive groups as they lie in memory.
+// Loading looks at nothing that it loads and does not branch: a conversion, or a copy
+// where two paths meet, would wait for every load that is under way. (Sixteen-bit
+// scales are loaded twice, and where there are no zeros the caller has other bytes
+// stand in for them.)
+template <int N>
+struct Scales4 {
+    uint32_t lo[N / 2], hi[N / 2];  // fp32: one after the other
+    uint32_t zero[(N + 3) / 4];
+    __device__ inline void load(global_t s, int type, global_t z) {
+        load_raw<2 * N>(lo, s);
+        load_raw<2 * N>(hi, s + (type == K3G_F32 ? 2 * N : 0));
+        load_raw<N>(zero, z);
+    }
+    __device__ inline float scale(int i, int type) const {
+        const uint32_t word = i < N / 2 ? lo[i] : hi[i - N / 2], half = lo[i / 2] >> (i % 2 * 16) & 0xFFFFu;
+        const float f16 = (float)__builtin_bit_cast(_Float16, (uint16_t)half);
+        return type == K3G_F16 ? f16 : __builtin_bit_cast(float, type == K3G_F32 ? word : half << 16);
+    }
+    __device__ inline uint32_t zero_at(int i) const { return zero[i / 4] >> (i % 4 * 8) & 0xFFu; }
+};
+
 __device__ inline void store_out(void *y, int type, int64_t i, float v) {
     if (type == K3G_F32)
         ((float *)y)[i] = v;

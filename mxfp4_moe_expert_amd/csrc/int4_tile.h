@@ -71,8 +71,8 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
 #pragma unroll
         for (int t = 0; t < TILES; ++t) at[t] = (uint32_t)(max(min(16 * (t % RT) + lr, left), 0) * pitch);
         const uint8_t *w0 = a.w[0] + first * pitch, *w1 = a.w[NW - 1] + first * pitch;
-        const int own = lane / (16 * RT);  // the weight whose scales this lane brings
-        const int64_t own_row = (first + max(min(lane % (16 * RT), left), 0)) * a.G;
+        const int own = lane / (16 * RT);  // the weight whose scales this lane brings, and its row's groups from the first row's
+        const int own_at = max(min(lane % (16 * RT), left), 0) * a.G;
         const int nf = (it.n_tok + 15) / 16;
         float4_t acc[TILES][NJ];
 #pragma unroll
@@ -81,31 +81,44 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             for (int j = 0; j < NJ; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
         uint4 w[TILES];
         Raw4<XT> xr[DMA ? 1 : PARTS];
-        float s[NG];
-        uint8_t z[NG];
+        Scales4<NG> s;
+        int s_shift = 0;  // its first groups that belong to the turn before
         auto load_w = [&](int step) {
             const uint32_t c = 16u * (uint32_t)min(4 * step + lq, units - 1);
 #pragma unroll
             for (int t = 0; t < TILES; ++t) w[t] = load16((t < RT ? w0 : w1) + (at[t] + c));
         };
+        // The bases are made anew each time (the empty assembly hides them): kept, the lanes' addresses would not fit the
+        // registers, and a reload from scratch memory waits for every load under way.
         auto load_s = [&](int turn) {
-            const void *sp = a.s[NW == 2 ? own : 0];
-            const uint8_t *zp = a.z[NW == 2 ? own : 0];
-            const int g0 = turn * NG;
+            const int g0 = turn * NG, from = max(min(g0, a.G - NG), 0), size = a.s_type == K3G_F32 ? 4 : 2;
+            s_shift = g0 - from;
+            global_t sb[NW], zb[NW];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) z[g] = 8;
-            if (g0 + NG <= a.G) {
-                scales_at<NG>(s, sp, a.s_type, own_row + g0);
-                if (zp) __builtin_memcpy(z, zp + own_row + g0, NG);
-            } else {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const int64_t i = own_row + min(g0 + g, a.G - 1);
-                    s[g] = scale_at(sp, a.s_type, i);
-                    if (zp) z[g] = zp[i];
-                }
+            for (int k = 0; k < NW; ++k) {
+                sb[k] = (global_t)a.s[k] + size * (first * a.G + from);
+                zb[k] = (a.z[k] ? (global_t)a.z[k] : (global_t)a.s[k]) + (first * a.G + from);
+                __asm__ volatile("" : "+s"(sb[k]), "+s"(zb[k]));
             }
+            s.load((own ? sb[NW - 1] : sb[0]) + size * own_at, a.s_type, (own ? zb[NW - 1] : zb[0]) + own_at);
         };
+        const bool given = a.z[NW == 2 ? own : 0];
+        auto put_s = [&]() {
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                if (g >= s_shift) {
+                    scales[(g - s_shift) * kWave + lane] = s.scale(g, a.s_type);
+                    zeros[(g - s_shift) * kWave + lane] = given ? (uint8_t)s.zero_at(g) : 8;
+                }
+        };
+        const bool short_row = a.G < NG;  // its groups go to LDS here, one by one
+        if (short_row) {
+            const int64_t at0 = first * a.G + own_at;
+            for (int g = 0; g < a.G; ++g) {
+                scales[g * kWave + lane] = scale_at(a.s[NW == 2 ? own : 0], a.s_type, at0 + g);
+                zeros[g * kWave + lane] = given ? a.z[NW == 2 ? own : 0][at0 + g] : 8;
+            }
+        }
         // chunk tid % 16 of every 16th row from tid / 16 on
         auto load_x = [&](int step) {
 #pragma unroll
@@ -135,19 +148,16 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             }
         };
         __syncthreads();  // src; and the stages are free
-        load_s(0);
+        if (!short_row) load_s(0);
         load_w(0);
         load_x(0);
         for (int step = 0; step < S; ++step) {
             put_x(step);
-            if constexpr (DMA) wait_vm<0>();
-            if (step % 2 == 0) {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    scales[g * kWave + lane] = s[g];
-                    zeros[g * kWave + lane] = z[g];
-                }
-            }
+            // Everything that was asked for a step ago is there (a wait that the compiler knows of: else it would wait again,
+            // for the loads that follow, where it first uses a register that it had reloaded before the loop).
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+            __asm__ volatile("" : : : "memory");
+            if (step % 2 == 0 && !short_row) put_s();
             // this step's codes in operand order, before the registers are loaded again
             uint32_t d[TILES][4];
 #pragma unroll
@@ -158,8 +168,8 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             }
             __syncthreads();
             if (step + 1 < S) {
-                if (step % 2 == 0 && step + 2 < S) load_s(step / 2 + 1);
                 load_x(step + 1);
+                if (step % 2 == 0 && step + 2 < S) load_s(step / 2 + 1);
             }
             const uint8_t *x0 = stage + (step & 1) * STEP + r * 256;
 #pragma unroll
@@ -218,34 +228,24 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
                 if (b == 4 - 2 * SPAN && step + 1 < S) load_w(step + 1);
             }
         }
-        // The way out. Outputs go 16 tokens at a time through the wavefront's own part of the stages, so that four lanes
-        // write a token's side by side (512 tokens of 512 -> 512: 27 us to 19); h, whose SiTU takes longer than its
-        // stores, goes straight (16384 rows of 256 experts: 1.65 ms, through LDS 1.86).
+        // The way out: 16 tokens at a time through the wavefront's own part of the stages, so that four lanes write a
+        // token's outputs side by side (4096 tokens of 512 -> 512: 27 us with two bytes a lane, so 19).
         __syncthreads();  // the stages have been read
         constexpr int PITCH = 16 * RT + 4;  // 4 more: the four lane rows write to different banks
         float *out = (float *)stage + wave * 16 * PITCH;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             if (j < nf) {
-                if constexpr (MODE == GLU) {
 #pragma unroll
-                    for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = 16 * j + 4 * q + i, row = m + 16 * t + r;
-                            const float y = situ(acc[t][j][i], acc[RT + t][j][i]);
-                            if (tok < it.n_tok && row < a.rows) store_out(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, y);
-                        }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) out[(4 * q + i) * PITCH + 16 * t + r] = acc[t][j][i];
-                    const int tok = 16 * j + lr, row = m + 4 * RT * lq;
-                    float v[4 * RT];
-                    __builtin_memcpy(v, out + lr * PITCH + 4 * RT * lq, sizeof v);
-                    if (tok < it.n_tok) store_outs<4 * RT>(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, a.rows - row, v);
-                }
+                    for (int i = 0; i < 4; ++i)
+                        out[(4 * q + i) * PITCH + 16 * t + r] =
+                            MODE == GLU ? situ(acc[t][j][i], acc[TILES - RT + t][j][i]) : acc[t][j][i];
+                const int tok = 16 * j + lr, row = m + 4 * RT * lq;
+                float v[4 * RT];
+                __builtin_memcpy(v, out + lr * PITCH + 4 * RT * lq, sizeof v);
+                if (tok < it.n_tok) store_outs<4 * RT>(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, a.rows - row, v);
             }
         }
     }
