@@ -112,24 +112,54 @@ def test_weights_of_value_zero_next_to_large_entries(k3g):
 def test_not_finite(k3g):
     """A token with an infinity or a NaN has no finite output; the tokens beside it keep theirs. So do rows with such
     a scale, and the rows beside them."""
-    for T in (5, 40, 300):
+    for T, n_out in ((1, 70), (5, 70), (40, 70), (300, 70), (300, 11000)):
         for xt in TYPES:
             g = gen(T)
-            w = ref.random_weights(g, (70,), 384, 32, torch.float32, True)
+            w = ref.random_weights(g, (n_out,), 384, 32, torch.float32, True)
             x = torch.randn(T, 384, device="cuda", generator=g).to(xt)
-            good = torch.empty(T, 70, device="cuda")
+            good = torch.empty(T, n_out, device="cuda")
             k3g.k3g_int4_matmul(good, x, k3g.int4(*w))
-            x[1, 7], x[T - 1, 380], x[3, 100] = float("inf"), float("nan"), -float("inf")
-            y = torch.empty(T, 70, device="cuda")
+            bad = sorted({T // 4, T // 2, T - 1})
+            for t, c, v in zip(bad, (7, 380, 100), (float("inf"), float("nan"), -float("inf"))):
+                x[t, c] = v
+            y = torch.empty(T, n_out, device="cuda")
             k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
             hit = torch.zeros(T, dtype=torch.bool, device="cuda")
-            hit[[1, 3, T - 1]] = True
+            hit[bad] = True
             assert not torch.isfinite(y[hit]).any() and torch.equal(y[~hit], good[~hit])
-            w[1][11, 4], w[1][69, 0] = float("nan"), float("inf")
+            w[1][11, 4], w[1][n_out - 1, 0] = float("nan"), float("inf")
             k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
-            rows = torch.ones(70, dtype=torch.bool, device="cuda")
-            rows[[11, 69]] = False
+            rows = torch.ones(n_out, dtype=torch.bool, device="cuda")
+            rows[[11, n_out - 1]] = False
             assert torch.equal(y[~hit][:, rows], good[~hit][:, rows]) and not torch.isfinite(y[:, ~rows]).any()
+
+
+@pytest.mark.parametrize("xt,least", [(torch.float32, 2.0 ** -126), (torch.bfloat16, 2.0 ** -133), (torch.float16, 2.0 ** -24)], ids=name)
+def test_the_smallest_entries(k3g, xt, least):
+    """Whole multiples of the type's smallest step (of fp32's smallest normal number), subnormal numbers for the most
+    part: products and sums are multiples of the same step below 2^24 of it, so nothing is rounded or lost."""
+    for T, n_out in ((1, 40), (3, 40), (50, 40), (300, 11000)):
+        g = gen(T)
+        w = ref.random_weights(g, (n_out,), 96, 32, torch.float32, True)
+        w[1].fill_(1.0)
+        x = (torch.randint(-9, 10, (T, 96), device="cuda", generator=g).double() * least).to(xt)
+        y = torch.empty(T, n_out, device="cuda")
+        k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
+        assert torch.equal(y.double(), x.double() @ ref.values(*w)[0].t().contiguous()), T
+
+
+def test_rows_in_slices_of_one_buffer(k3g):
+    """x and y beside each other in the rows of one buffer."""
+    n, rows = 256, 72
+    for T in (1, 9, 70):
+        g = gen(T)
+        w = ref.random_weights(g, (rows,), n, 64, torch.bfloat16, True, exact=True)
+        b = torch.full((T, n + rows + 5), 7.0, device="cuda")
+        b[:, :n] = torch.randint(-4, 5, (T, n), device="cuda", generator=g).float()
+        x, y = b[:, :n], b[:, n + 2:n + 2 + rows]
+        want = x.double() @ ref.values(*w)[0].t().contiguous()
+        k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
+        assert torch.equal(y.double(), want) and bool((b[:, n:n + 2] == 7).all() and (b[:, n + 2 + rows:] == 7).all())
 
 
 def test_zeros_at_both_ends_and_tensors_off_their_alignment(k3g):
