@@ -7,6 +7,9 @@
 // s and z are one number a lane. gfx950's scaled convert turns two codes at a time
 // into fp32 (see int4.h: a code is n 2^-9 in e4m3), 15 instructions for eight weights
 // with their multiply-adds; the wavefront's sum over its lanes ends a weight row.
+// A token's 16 experts of 3584 x 3072, groups of 32: gated up-products 41 us (5.1 TB/s), w2 25
+// (4.2: 96 pieces a row leave a quarter of two wavefronts' lanes empty); one token 7168
+// -> 3584 8 us, latency.
 #include "int4.h"
 
 namespace k3g {

@@ -11,6 +11,14 @@
 // of a row; a permutation over the wavefront and a transposition of the four
 // 16-lane rows bring the dword of (output r, columns 8q ..) of each of the four
 // blocks into place.
+//
+// Where there are items enough (8192), a wavefront takes one to itself, the row's
+// length turn after turn, and 16 of them a CU keep loads under way without a barrier
+// between them: 1024 rows over 323 experts of 3584 x 3072, gated up-products 0.98 ms against
+// 1.26 split, w2 0.49 against 0.88 (3.9 TB/s; a wavefront's loads and products take
+// turns). Split, one bf16 token's worth of codes is latency: 7168 -> 3584, 2 tokens 9.5 us,
+// 16 tokens 11.4; 32 tokens 14 us. 61 fp32 tokens 3584 -> 7168 24 us: vector work, most of
+// it the split of x into bf16 parts by every workgroup.
 #pragma once
 
 #include "int4.h"

@@ -3,6 +3,13 @@
 // wavefronts. The activations come through LDS in steps of 128 columns, two
 // steps' places; each wavefront loads its own codes a step ahead and makes operands
 // of them in registers, once for all of the tile's tokens.
+//
+// A step of 128 columns is 128 matrix and about 650 vector instructions a wavefront
+// at groups of 64: 304 make operands of 8192 codes, 256 apply the groups' scales to
+// the partial sums. Issue bounds it: 4096 tokens 7168 -> 6144 393-410 us, 0.88-0.92
+// PFLOP/s, matrix cores 31-36% busy; 65536 rows over 536 experts of 3584 x 3072 2.8 ms,
+// their gated up-products 6.1. Two workgroups a CU take each other's waits: one alone
+// needs 0.7 of the time of two.
 #pragma once
 
 #include "int4.h"

@@ -1,5 +1,6 @@
 // mx.h -- what the microscaled-activation kernels share (mx.hip, mxmm.hip):
-// group scales and codes, element types, and the host-side checks.
+// group scales and codes, element types, and the host-side checks; of these the
+// element types, sums and checks serve the routed pairs and the int4 products too.
 #pragma once
 
 #include <math.h>
