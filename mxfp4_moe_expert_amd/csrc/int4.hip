@@ -38,9 +38,12 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 // fp32 (64 tokens a tile) 7168 -> 3584, 512 tokens (112) 144, 219, 1024 (224) 253, 222. Grouped, by the average rows of the
 // bank's experts: 256 of 3584 x 3584, bf16, 16 rows 584, 623, 32 rows 873, 698; fp32 64 rows 635, 684, 128 rows 1133, 1025.
 //
-// Streamed, 64 outputs by 32 tokens, or 32 by 16 where that leaves half a tile empty: 7168 -> 3584, 32 tokens (32 x
-// 16 first) 14, 27, 64 tokens 22, 26, 96 30, 26 (3584 -> 7168: 19, 20; 34, 20); grouped 256 x 4 rows 467, 525, 16 rows 725,
-// 584. Up to 16 tokens of few outputs take 16 a workgroup: 7168 -> 3584, 16 tokens 11, 14; 3584 -> 7168 12, 11. Where
+// Streamed, 64 outputs by 32 tokens, or 32 by 16 where half a tile would be empty or where those are at most two
+// workgroups a CU, which run at once (32 x 16 first; bf16, fp32 in brackets): 7168 -> 3584, 64 tokens (448) 23, 31 (34, 40),
+// 80 (560) 33, 28 (50, 37); 3584 -> 7168, 32 (448) 15, 20 (21, 26), 33 (672) 20, 18 (27, 25); 4096 -> 1024, 128 (256) 9.7, 17
+// (14, 25); 3584 -> 14336, 16 (448) 15, 18 (21, 21), 17 23, 20 (36, 26). Grouped, 256 of 3584 x 3584, 9 rows 575, 650 (896,
+// 799), 11 rows 591, 659, 14 rows 694, 696; fp32 8 rows 837, 890. Up to 16 tokens of few outputs take 16 a workgroup: 7168 ->
+// 3584, 16 tokens 13, 16; 3584 -> 7168 12, 11. Where
 // 64 x 32 would be more than a workgroup a CU, bf16 and fp16 take 64 x 64: 7168 -> 3584, 128 tokens (224) 25, 39, 192 47,
 // 38, 512 91, 71; 3584 -> 7168, 64 tokens (224) 20, 29, 128 36, 29 (fp32 49, 55; 512 tokens 162, 206).
 int product_form(const I4Args &a, int mode, int x_type) {
@@ -51,7 +54,9 @@ int product_form(const I4Args &a, int mode, int x_type) {
     const int64_t items = ((int64_t)a.rows + 255) / 256 * tiles * (mode == GLU ? 2 : 1);
     if (n > (wide ? 20 : 80) && items >= (wide ? 128 : 160)) return wide ? form(256, 128) : form(256, 64);
     if (mode == DENSE && a.T <= 16 && a.rows <= 16 * 256) return form(16, 16);
-    if (n <= (mode == DENSE ? 32 : 8)) return form(32, 16);
+    const bool few = mode == DENSE ? n <= 16 || ((int64_t)a.rows + 31) / 32 * ((n + 15) / 16) <= 512
+                                   : n <= (x_type == K3G_F32 ? 8 : 12);
+    if (few) return form(32, 16);
     return mode == DENSE && x_type != K3G_F32 && (a.rows + 63) / 64 * ((n + 31) / 32) > 256 ? form(64, 64) : form(64, 32);
 }
 

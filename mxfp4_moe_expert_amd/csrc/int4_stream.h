@@ -1,6 +1,6 @@
 // int4_stream.h -- int4 products whose weights are streamed once: a workgroup
 // takes 16 NT rows of activations and 16 RT outputs (of one expert) and splits
-// the row's length over its wavefronts, 512 columns at a time (256 of four tiles), whose
+// the row's length over its wavefronts, 512 or 256 columns at a time, whose
 // codes and scales are all in flight before the first product. The wavefronts' sums meet in
 // LDS and are added in wavefront order.
 //
@@ -26,13 +26,17 @@
 namespace k3g {
 
 constexpr int kI4Waves = 8;
-constexpr int i4_stream_occupancy(int xt, int group, int tiles) { return tiles > 2 || xt == K3G_F32 ? 2 : group == 32 ? 3 : 4; }  // wavefronts a SIMD
-constexpr int i4_stream_steps(int tiles) { return tiles > 2 ? 2 : 4; }
+constexpr int i4_stream_occupancy(int tiles) { return tiles > 2 ? 2 : 4; }  // wavefronts a SIMD
+// Steps of 128 columns that are loaded together. Two tiles: what lets 128 registers do, so that a CU holds two
+// workgroups. Groups of 32 by four steps, at two wavefronts a SIMD (fp32; bf16 at three), 256 experts of 3584 x 3584 by 1024
+// rows 1137 us (bf16 622), so 809 (516), their gated up-products 2169 (1143), 1559 (969); fp32 groups of 64 at three 1062, 773;
+// bf16 groups of 64 by two steps 445, by four 426.
+constexpr int i4_stream_steps(int tiles, int group) { return tiles > 2 || (group == 32 && tiles > 1) ? 2 : 4; }
 
 template <int XT, int GROUP, int MODE, int RT, int NT>
-__global__ __launch_bounds__(kI4Waves * kWave, i4_stream_occupancy(XT, GROUP, RT * (MODE == GLU ? 2 : 1) * NT)) void int4_stream_kernel(I4Args a) {
+__global__ __launch_bounds__(kI4Waves * kWave, i4_stream_occupancy(RT * (MODE == GLU ? 2 : 1) * NT)) void int4_stream_kernel(I4Args a) {
     constexpr int NW = MODE == GLU ? 2 : 1, TILES = RT * NW;
-    constexpr int STEPS = i4_stream_steps(TILES);                          // of 128 columns that are loaded together
+    constexpr int STEPS = i4_stream_steps(TILES, GROUP);
     constexpr int SPAN = XT == K3G_F32 || GROUP == 32 ? 1 : 2;             // blocks of 32 columns between two additions
     constexpr int NG = 128 * STEPS / GROUP;                                // groups of a turn
     constexpr int X = XT == K3G_F32 ? 4 : 2;
@@ -178,7 +182,8 @@ __global__ __launch_bounds__(kI4Waves * kWave, i4_stream_occupancy(XT, GROUP, RT
 template <int XT, int GROUP, int MODE, int RT, int NT>
 int launch_int4_stream(const I4Args &a, hipStream_t st) {
     constexpr int TILES = RT * (MODE == GLU ? 2 : 1);
-    const int turns = (a.in / 32 + 4 * i4_stream_steps(TILES) - 1) / (4 * i4_stream_steps(TILES));
+    constexpr int UNITS = 4 * i4_stream_steps(TILES, GROUP);
+    const int turns = (a.in / 32 + UNITS - 1) / UNITS;
     const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 16 * NT - 1) / (16 * NT)
                                         : (int64_t)a.T / (16 * NT) + (a.E < a.T ? a.E : a.T);
     const int64_t items = ((int64_t)a.rows + 16 * RT - 1) / (16 * RT) * tiles;

@@ -86,11 +86,15 @@ def test_form(k3g):
     f32, b16, form = torch.float32, torch.bfloat16, k3g.k3g_probe_int4_form
     assert form(b16, 1, 3584, 7168) == (8, 1) and form(b16, 1, 8, 65536) == (16, 16)
     assert form(b16, 16, 3584, 7168) == (16, 16) and form(b16, 16, 7168, 3584) == (32, 16)
-    assert form(b16, 33, 3584, 7168) == (64, 32) and form(b16, 1536, 3584, 7168) == (256, 128)
+    assert form(b16, 64, 3584, 7168) == (32, 16) and form(b16, 65, 3584, 7168) == (64, 32)
+    assert form(f32, 32, 8192, 64) == (32, 16) and form(f32, 32, 8193, 64) == (64, 32) == form(f32, 17, 16384, 64)
+    assert form(b16, 1536, 3584, 7168) == (256, 128)
     assert form(b16, 1024, 3584, 7168, aligned=False) == (256, 64) and form(f32, 1024, 3584, 7168) == (256, 64)
     assert form(f32, 512, 3584, 7168) == (64, 32) and form(b16, 512, 3584, 7168) == (64, 64)
     assert form(b16, 128, 3584, 7168) == (64, 32) and form(b16, 129, 3584, 7168) == (64, 64)
     assert form(f32, 16, 3072, 3584, 896, glu=True) == (8, 1) and form(b16, 1024, 3072, 3584, 896, glu=True) == (32, 16)
+    assert form(b16, 12 * 896, 3584, 3072, 896) == (32, 16) and form(b16, 12 * 896 + 1, 3584, 3072, 896) == (64, 32)
+    assert form(f32, 8 * 896, 3584, 3072, 896) == (32, 16) and form(f32, 8 * 896 + 1, 3584, 3072, 896) == (64, 32)
     assert form(b16, 16 * 896, 3584, 3072, 896) == (64, 32) and form(b16, 65536, 3584, 3072, 896) == (256, 128)
     L = k3g.lib()
     ok = [1, 1, 1, 64, 64, 64, 8]
