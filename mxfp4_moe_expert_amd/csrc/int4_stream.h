@@ -12,13 +12,15 @@
 // 16-lane rows bring the dword of (output r, columns 8q ..) of each of the four
 // blocks into place.
 //
-// Where there are items enough (8192), a wavefront takes one to itself, the row's
-// length turn after turn, and 16 of them a CU keep loads under way without a barrier
-// between them: 1024 rows over 323 experts of 3584 x 3072, gated up-products 0.98 ms against
+// Where there is an item for each of 16 wavefronts a CU (4096), a wavefront takes one to
+// itself, the row's length turn after turn, and they keep loads under way without a
+// barrier between them: 1024 rows over 323 experts of 3584 x 3072, gated up-products 0.98 ms against
 // 1.26 split, w2 0.49 against 0.88 (3.9 TB/s; a wavefront's loads and products take
-// turns). Split, one bf16 token's worth of codes is latency: 7168 -> 3584, 2 tokens 9.5 us,
-// 16 tokens 11.4; 32 tokens 14 us. 61 fp32 tokens 3584 -> 7168 24 us: vector work, most of
-// it the split of x into bf16 parts by every workgroup.
+// turns); 500 bf16 rows over 64 experts of 1024 x 3584 (6,080 items at most) 58 us against
+// 82, fp32 109, 135; 24 fp32 rows over 16 of 2048 x 7168 (2,176) 136 us, split 100. Split, one bf16 token's worth of codes is latency: 7168 -> 3584, 2 tokens 9.5 us,
+// 16 tokens 11.4; 32 tokens 14 us. 61 fp32 tokens 3584 -> 7168 24 us: the wavefronts wait
+// for loads 44% of the time (two turns' codes, and x from L2), and the vector units, busy
+// 53%, have a third of their work in splitting x into bf16 parts.
 #pragma once
 
 #include "int4.h"
@@ -187,7 +189,7 @@ int launch_int4_stream(const I4Args &a, hipStream_t st) {
     const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 16 * NT - 1) / (16 * NT)
                                         : (int64_t)a.T / (16 * NT) + (a.E < a.T ? a.E : a.T);
     const int64_t items = ((int64_t)a.rows + 16 * RT - 1) / (16 * RT) * tiles;
-    const bool alone = items >= 8192;
+    const bool alone = items >= 4096;
     const int waves = alone ? 1 : turns < kI4Waves ? turns : kI4Waves;
     const int64_t most = alone ? 4096 : 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
     size_t lds = (size_t)waves * TILES * NT * kWave * 16 + (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
