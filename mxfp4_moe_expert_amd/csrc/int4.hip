@@ -28,9 +28,11 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 
 // The kernel of a product: weight rows << 16 | tokens of its tile; the vector kernel's is 8 << 16 | 1.
 //
-// A single row runs on the vector units, and so do the few of a token's experts, whose groups hold about one row
-// each (us; vector, streamed): one bf16 token 7168 -> 3584 8.6, 9.4; two 9.7, 9.5 (fp32 3584 -> 7168 8.8, 13.5; 11.1,
-// 13.6); 64 rows of 256 experts 88, 135; 256 rows 290, 250.
+// A single row runs on the vector units, and so do two of fp32, and rows of experts, a workgroup's row each, where
+// few experts would have two (us; vector, streamed): one bf16 token 7168 -> 3584 8.6, 9.4; two 9.7, 9.5, fp32 9.8, 16, three
+// 15, 16. Of 256 experts of 3584 x 3584, groups of 32, 64 rows 91, 132, 128 rows 149, 215, 256 286, 307 (groups of 128 145, 173
+// by 128, 213, 205 by 192); fp32 128 rows 150, 351, 256 279, 483. More than 256 rows are streamed: rows that crowd
+// on one expert cost this kernel what rows of many do.
 //
 // Tiles of 256 outputs pay where rows are many and items enough to fill half of the chip (streamed, tiled): bf16 3584
 // -> 7168, 512 tokens (112 items) 100, 100, 1024 tokens (224) 182, 102; 7168 -> 3584, 1024 tokens (112) 138, 185, 1536
@@ -47,17 +49,19 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 // 64 x 32 would be more than a workgroup a CU, bf16 and fp16 take 64 x 64: 7168 -> 3584, 128 tokens (224) 25, 39, 192 47,
 // 38, 512 91, 71; 3584 -> 7168, 64 tokens (224) 20, 29, 128 36, 29 (fp32 49, 55; 512 tokens 162, 206).
 int product_form(const I4Args &a, int mode, int x_type) {
-    if (a.in <= kGvMaxIn && (a.T == 1 || (mode != DENSE && a.T <= 64 && 2 * a.T <= a.E))) return form(8, 1);
-    const bool wide = x_type != K3G_F32 && a.x_vec;
+    const bool f32 = x_type == K3G_F32;
+    const bool spread = a.T <= 256 && (f32 ? a.T : 2 * a.T) <= a.E &&
+                        (int64_t)a.rows * a.T <= kMaxRows;  // (its grid is of fewer than 2^32 threads)
+    if (a.in <= kGvMaxIn && (a.T == 1 || (mode == DENSE ? f32 && a.T == 2 : spread))) return form(8, 1);
+    const bool wide = !f32 && a.x_vec;
     const int64_t n = mode == DENSE ? a.T : ((int64_t)a.T + a.E - 1) / a.E, most = wide ? 128 : 64;
     const int64_t tiles = mode == DENSE ? (n + most - 1) / most : (n + most - 1) / most * (a.E < a.T ? a.E : a.T);
     const int64_t items = ((int64_t)a.rows + 255) / 256 * tiles * (mode == GLU ? 2 : 1);
     if (n > (wide ? 20 : 80) && items >= (wide ? 128 : 160)) return wide ? form(256, 128) : form(256, 64);
     if (mode == DENSE && a.T <= 16 && a.rows <= 16 * 256) return form(16, 16);
-    const bool few = mode == DENSE ? n <= 16 || ((int64_t)a.rows + 31) / 32 * ((n + 15) / 16) <= 512
-                                   : n <= (x_type == K3G_F32 ? 8 : 12);
+    const bool few = mode == DENSE ? n <= 16 || ((int64_t)a.rows + 31) / 32 * ((n + 15) / 16) <= 512 : n <= (f32 ? 8 : 12);
     if (few) return form(32, 16);
-    return mode == DENSE && x_type != K3G_F32 && (a.rows + 63) / 64 * ((n + 31) / 32) > 256 ? form(64, 64) : form(64, 32);
+    return mode == DENSE && !f32 && (a.rows + 63) / 64 * ((n + 31) / 32) > 256 ? form(64, 64) : form(64, 32);
 }
 
 int launch(I4Args &a, int mode, int x_type, int group, void *stream) {

@@ -1,5 +1,5 @@
 // int4_gemv.hip -- products of single rows with int4 weights, on the vector units:
-// one token, or the few rows of a token's experts.
+// one token, or the rows of a few tokens' experts.
 //
 // y[r] = sum over the row's 32-column pieces of s (sum n x - z sum x): a lane holds
 // 32 columns of x in fp32, and their sum, for each 2048 columns of its wavefront's

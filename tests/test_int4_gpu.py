@@ -37,7 +37,7 @@ DENSE = [(1, 32, 1, 32), (1, 64, 17, 64), (1, 128, 16, 128), (2, 96, 33, 32), (1
          (15, 544, 31, 32), (16, 640, 64, 128), (17, 1056, 48, 32), (31, 4224, 40, 128), (33, 3584, 129, 64),
          (61, 3584, 7168, 32), (64, 4160, 257, 32), (65, 512, 130, 128), (127, 1120, 77, 32), (200, 2048, 300, 64),
          (129, 352, 4200, 32), (141, 704, 4500, 64),
-         (33, 704, 8300, 64), (24, 640, 8300, 128), (250, 1056, 500, 32), (70, 1088, 777, 64), (257, 2176, 70, 128),
+         (33, 704, 8300, 64), (2, 4224, 1030, 64), (24, 640, 8300, 128), (250, 1056, 500, 32), (70, 1088, 777, 64), (257, 2176, 70, 128),
          (4, 65536, 5, 32), (1000, 256, 512, 64), (300, 768, 4097, 128), (1, 34816, 40, 64),
          # tiles: ragged outputs and tokens, an odd number of 32-column blocks, ends inside a turn of 256 columns
          (300, 352, 11001, 32), (515, 704, 6700, 64), (500, 640, 11000, 128), (385, 32, 9700, 32)]
@@ -221,7 +221,8 @@ GROUPED = [(1, 5, 64, 16, 32, 1), (7, 40, 128, 48, 64, 2), (896, 64, 96, 33, 32,
            # tiles
            (16, 1500, 352, 2000, 32, 1), (12, 1400, 448, 2600, 64, 4), (13, 1300, 640, 2401, 128, 2),
            # the vector kernel: rows of experts, more rows than an expert's share
-           (896, 16, 3584, 100, 32, 16), (200, 64, 2112, 33, 64, 1), (130, 60, 6272, 70, 128, 7)]
+           (896, 16, 3584, 100, 32, 16), (200, 64, 2112, 33, 64, 1), (130, 60, 6272, 70, 128, 7),
+           (256, 250, 2080, 50, 32, 3), (600, 256, 1088, 33, 64, 4)]
 
 
 @pytest.mark.parametrize("xt", TYPES, ids=name)

@@ -93,6 +93,10 @@ def test_form(k3g):
     assert form(f32, 512, 3584, 7168) == (64, 32) and form(b16, 512, 3584, 7168) == (64, 64)
     assert form(b16, 128, 3584, 7168) == (64, 32) and form(b16, 129, 3584, 7168) == (64, 64)
     assert form(f32, 16, 3072, 3584, 896, glu=True) == (8, 1) and form(b16, 1024, 3072, 3584, 896, glu=True) == (32, 16)
+    assert form(f32, 2, 3584, 7168) == (8, 1) and form(f32, 3, 3584, 7168) == (16, 16) == form(b16, 2, 3584, 7168)
+    assert form(f32, 256, 3584, 512, 256) == (8, 1) and form(f32, 256, 3584, 512, 255) == (32, 16) == form(f32, 257, 64, 64, 896)
+    assert form(f32, 4, 2**28, 32, 4, glu=True) == (8, 1) and form(f32, 4, 2**28 + 1, 32, 4, glu=True) == (32, 16)
+    assert form(b16, 128, 3584, 512, 256) == (8, 1) and form(b16, 128, 3584, 512, 255) == (32, 16)
     assert form(b16, 12 * 896, 3584, 3072, 896) == (32, 16) and form(b16, 12 * 896 + 1, 3584, 3072, 896) == (64, 32)
     assert form(f32, 8 * 896, 3584, 3072, 896) == (32, 16) and form(f32, 8 * 896 + 1, 3584, 3072, 896) == (64, 32)
     assert form(b16, 16 * 896, 3584, 3072, 896) == (64, 32) and form(b16, 65536, 3584, 3072, 896) == (256, 128)
