@@ -361,10 +361,11 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
         }
         if (DOT) {
             __syncthreads();
-            for (int k = tid; k < n_pairs; k += a.waves * kWave) {
-                float d = part[k];
-                for (int w = 1; w < a.waves; ++w) d += part[w * kPairMaxTopK + k];
-                a.dwts[t * a.K + k0 + k] = d;
+            if (tid < n_pairs) {  // the first wavefront: lane k's pair is k
+                float d = part[tid];
+                for (int w = 1; w < a.waves; ++w) d += part[w * kPairMaxTopK + tid];
+                // a pair without a row was multiplied as zeros, which next to a token's infinity or NaN is no zero
+                a.dwts[t * a.K + k0 + tid] = mine < 0 ? 0.0f : d;
             }
             __syncthreads();
         }
