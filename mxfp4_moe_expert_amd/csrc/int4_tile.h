@@ -251,7 +251,9 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
                             MODE == GLU ? situ(acc[t][j][i], acc[TILES - RT + t][j][i]) : acc[t][j][i];
                 const int tok = 16 * j + lr, row = m + 4 * RT * lq;
                 float v[4 * RT];
+                wave_lds_order();
                 __builtin_memcpy(v, out + lr * PITCH + 4 * RT * lq, sizeof v);
+                wave_lds_order();  // the next 16 tokens' results go to the same place
                 if (tok < it.n_tok) store_outs<4 * RT>(a.y, a.y_type, (int64_t)(it.p + tok) * a.ys + row, a.rows - row, v);
             }
         }

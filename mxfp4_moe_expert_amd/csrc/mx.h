@@ -110,6 +110,14 @@ __device__ inline float wave_sum4(const float *y, int lane) {
     return __builtin_bit_cast(float, (uint32_t)t[0]) + __builtin_bit_cast(float, (uint32_t)t[1]);
 }
 
+// Between a wavefront's plain stores to LDS and its other lanes' loads of them: the hardware keeps their order, and
+// this keeps the compiler from moving a load that it believes to be of other memory above a store. No instruction.
+__device__ inline void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- host checks --------------------------------------------------------------------
 
 int device_ok();  // abi.hip

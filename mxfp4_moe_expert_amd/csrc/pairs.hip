@@ -159,12 +159,11 @@ __global__ __launch_bounds__(NT) void sort_kernel(int32_t *__restrict__ offsets,
                 same &= one ? m : ~m;
             }
             const uint64_t below = same & ((1ull << lane) - 1ull);
-            rank[s] = 0;
-            if (valid) {
-                const int n = mine[id[s]];
-                rank[s] = n + __popcll(below);
-                if (below == 0) mine[id[s]] = (uint16_t)(n + __popcll(same));
-            }
+            const int n = valid ? mine[id[s]] : 0;
+            rank[s] = n + __popcll(below);
+            wave_lds_order();  // all lanes of an expert read its counter before the first of them counts on
+            if (valid && below == 0) mine[id[s]] = (uint16_t)(n + __popcll(same));
+            wave_lds_order();
         }
         __syncthreads();
         for (int e = tid; e < E; e += NT) {
@@ -300,7 +299,10 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
         int mine = lane < n_pairs ? a.inv[t * a.K + k0 + lane] : -1;
         if ((unsigned)mine >= (unsigned)a.R) mine = -1;
         const float weight = mine < 0 ? 0.0f : a.wts ? a.wts[t * a.K + k0 + lane] : 1.0f;
-        if (DOT) part[wave * kPairMaxTopK + lane] = 0.0f;
+        if (DOT) {
+            part[wave * kPairMaxTopK + lane] = 0.0f;
+            wave_lds_order();  // other lanes add to them
+        }
         for (int c0 = (rest - turn * a.parts) * width; c0 < a.n; c0 += a.parts * width) {
             const int c = c0 + tid * kPairCols, n = a.n - c;
             float tok[kPairCols], sum[kPairCols] = {};
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(U > 4 ? 512 : 1024) void pairs_kernel(PairArgs a) {
                             for (int i = 0; i < kPairCols; ++i) d[m] = __builtin_fmaf(tok[i], v[j + m][i], d[m]);
                         }
                         const float all4 = wave_sum4(d, lane);
-                        if (lane < 4) part[wave * kPairMaxTopK + k + j + lane] += all4;
+                        if (lane < 4) part[wave * kPairMaxTopK + k + j + lane] += all4;  // (always by the same lane)
                     }
                 }
                 if (SCATTER) {
