@@ -551,7 +551,7 @@ int k3g_mx_grouped_glu(const k3g_mx *h, const k3g_mx *a, const k3g_expert_bank *
  *   packed [n_experts][rows][in/2]: codes n of 0 .. 15, two per byte, the LOW nibble
  *          is the even column;
  *   scales [n_experts][rows][in/group] of scale_type (a k3g_type);
- *   zeros  uint8 [n_experts][rows][in/group], each at most 128, or null: all 8;
+ *   zeros  uint8 [n_experts][rows][in/group], or null: all 8;
  * an element is (n - zero) * scale of its group. group 32, 64 or 128; in a positive
  * multiple of group, at most 65536; rows <= 2^30, n_experts <= 2048
  * (K3G_EUNSUPPORTED beyond). packed 16-byte aligned, scales to their type. */

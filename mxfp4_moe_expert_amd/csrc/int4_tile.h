@@ -21,7 +21,7 @@ namespace k3g {
 // next), the conversion one instruction an entry that reads a byte with its sign, and
 // the fp32 result's upper half is the bf16. 19 instructions; against codes8 it spares
 // the product with ones and the multiplication of every partial sum, which a
-// tile of this many tokens would spend more on.
+// tile of this many tokens would spend more on. Zeros up to 128: a larger one borrows.
 template <int XT>
 __device__ inline uint4 codes8(uint32_t d, uint32_t z4) {
     uint32_t lo = ((d & 0x0F0F0F0Fu) | 0x80808080u) - z4, hi = (((d >> 4) & 0x0F0F0F0Fu) | 0x80808080u) - z4;
@@ -30,6 +30,22 @@ __device__ inline uint4 codes8(uint32_t d, uint32_t z4) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const float e = (float)(int)(int8_t)(lo >> (8 * b)), o = (float)(int)(int8_t)(hi >> (8 * b));
+        if constexpr (XT == K3G_F16)
+            v[b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(e, o));
+        else
+            v[b] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, o), __builtin_bit_cast(uint32_t, e), 0x07060302u);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// The same less a zero of any byte, subtracted in fp32: eight instructions more (down to -255, so exact in bf16 too).
+// Taken for the turns of a wavefront that meet a zero of 128 or more; that branch costs the others 1 to 2% (4096 tokens
+// 7168 -> 6144, groups of 64, 391 us without it, 397 with).
+template <int XT>
+__device__ inline uint4 codes8_any(uint32_t d, float z) {
+    uint32_t v[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float e = (float)(d >> (8 * b) & 0xFu) - z, o = (float)(d >> (8 * b + 4) & 0xFu) - z;
         if constexpr (XT == K3G_F16)
             v[b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(e, o));
         else
@@ -110,7 +126,12 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             s.load((own ? sb[NW - 1] : sb[0]) + size * own_at, a.s_type, (own ? zb[NW - 1] : zb[0]) + own_at);
         };
         const bool given = a.z[NW == 2 ? own : 0];
+        bool far = false;  // a zero of the turn's groups is 128 or more
         auto put_s = [&]() {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < (NG + 3) / 4; ++i) top |= s.zero[i];
+            far = __ballot(given && (top & 0x80808080u)) != 0;
 #pragma unroll
             for (int g = 0; g < NG; ++g)
                 if (g >= s_shift) {
@@ -122,8 +143,10 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
         if (short_row) {
             const int64_t at0 = first * a.G + own_at;
             for (int g = 0; g < a.G; ++g) {
+                const uint8_t z = given ? a.z[NW == 2 ? own : 0][at0 + g] : 8;
                 scales[g * kWave + lane] = scale_at(a.s[NW == 2 ? own : 0], a.s_type, at0 + g);
-                zeros[g * kWave + lane] = given ? a.z[NW == 2 ? own : 0][at0 + g] : 8;
+                zeros[g * kWave + lane] = z;
+                far = far || __ballot(z > 127) != 0;
             }
         }
         // chunk tid % 16 of every 16th row from tid / 16 on
@@ -198,12 +221,22 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
                     };
                     uint4 codes[TILES][SPAN];
                     float sc[TILES];
+                    uint32_t zero[TILES];
 #pragma unroll
                     for (int t = 0; t < TILES; ++t) {
                         sc[t] = scales[g * kWave + 16 * t + r];
-                        const uint32_t z4 = zeros[g * kWave + 16 * t + r] * 0x01010101u;
+                        zero[t] = zeros[g * kWave + 16 * t + r];
+                    }
+                    if (__builtin_expect(far, 0)) {  // (around all tiles: a choice for each makes the call 10% longer)
 #pragma unroll
-                        for (int k = 0; k < SPAN; ++k) codes[t][k] = codes8<XT>(d[t][b + k], z4);
+                        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                            for (int k = 0; k < SPAN; ++k) codes[t][k] = codes8_any<XT>(d[t][b + k], (float)zero[t]);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                            for (int k = 0; k < SPAN; ++k) codes[t][k] = codes8<XT>(d[t][b + k], zero[t] * 0x01010101u);
                     }
                     // two token tiles at a time: the products of the second run as the sums of the first are added
 #pragma unroll

@@ -1,0 +1,118 @@
+"""Every kernel of the int4 products, by sizes that each asserts to select it: zeros of any byte."""
+import pytest
+import torch
+
+from tests import int4_ref as ref
+
+pytestmark = pytest.mark.gpu
+TYPES = ref.TYPES
+F32, B16, F16 = TYPES
+name = lambda t: str(t)[6:] if isinstance(t, torch.dtype) else None  # noqa: E731
+
+
+@pytest.fixture(scope="module")
+def k3g():
+    import mxfp4_moe_expert_amd as k
+    return k
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rows_at(x, aligned):
+    """x's rows on 16-byte addresses, or the same rows off them (fp32 rows are always on 4-byte ones)."""
+    if aligned:
+        return x.contiguous()
+    b = torch.zeros(x.numel() + x.shape[0] + 1, dtype=x.dtype, device="cuda")
+    v = b[1:].view(x.shape[0], -1)[:, :x.shape[1]]
+    return v.copy_(x)
+
+
+def forms(xt, n):
+    """(form, aligned, experts (0: dense), rows of y, outputs) that reach every kernel with rows of n columns (n at most
+    2048: the rule goes by other sizes), dense and grouped."""
+    wide = [((256, 64), True)] if xt == F32 else [((256, 128), True), ((256, 64), False)]
+    dense = [((8, 1), True, 1, 70), ((16, 16), True, 7, 130), ((32, 16), True, 9, 4200), ((64, 32), True, 33, 7000)]
+    dense += [] if xt == F32 else [((64, 64), True, 141, 4500)]
+    dense += [(f, a, 385, 10753) for f, a in wide]
+    grouped = [((8, 1), True, 40, 20, 70), ((32, 16), True, 5, 37, 70), ((64, 32), True, 4, 70, 100)]
+    grouped += [(f, a, 4, 1300, 2700) for f, a in wide]
+    return [(f, a, 0, T, rows) for f, a, T, rows in dense] + grouped
+
+
+def product(k3g, form, aligned, E, T, rows, n, x, *w, off=None, perm=None, top_k=1, mark=7.0):
+    """The product's output in fp32, its kernel asserted; E = 0: dense."""
+    assert k3g.k3g_probe_int4_form(x.dtype, T, rows, n, E, aligned=aligned) == form
+    x = rows_at(x, aligned)
+    assert (x.data_ptr() % 16 == 0 and (x.shape[0] == 1 or x.stride(0) * x.element_size() % 16 == 0)) == aligned
+    b = torch.full((T + 2, rows + 3), mark, device="cuda")
+    y = b[1:T + 1, 1:rows + 1]
+    if E:
+        k3g.k3g_int4_grouped_matmul(y, x, k3g.int4(*w), off, perm=perm, top_k=top_k)
+    else:
+        k3g.k3g_int4_matmul(y, x, k3g.int4(*w))
+    assert bool((b[[0, -1]] == mark).all() and (b[:, [0, -1, -2]] == mark).all())
+    return y
+
+
+def even(E, T):
+    """Offsets of E groups of about as many rows, and the expert of each row."""
+    off = (torch.arange(E + 1, device="cuda") * T // E).int()
+    return off, torch.bucketize(torch.arange(T, device="cuda"), off[1:].long(), right=True)
+
+
+def expect(x, w, E, T, expert):
+    """The product in 64 bits and its magnitudes."""
+    if not E:
+        v, m = ref.values(*w)
+        return x.double() @ v.t().contiguous(), x.double().abs() @ m.t().contiguous()
+    rows = w[0].shape[1]
+    want, mag = [torch.empty(T, rows, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for e in range(E):
+        s = expert == e
+        v, m = ref.values(*[None if t is None else t[e] for t in w])
+        want[s], mag[s] = x[s].double() @ v.t().contiguous(), x[s].double().abs() @ m.t().contiguous()
+    return want, mag
+
+
+def any_zeros(g, lead, n, group):
+    """Weights with zeros of any byte, every range's ends among them, and scales that are powers of two."""
+    packed, s, _ = ref.random_weights(g, lead, n, group, B16, False, exact=True)
+    z = torch.randint(0, 256, s.shape, dtype=torch.uint8, device="cuda", generator=g)
+    ends = torch.tensor([0, 15, 127, 128, 129, 143, 144, 255], dtype=torch.uint8, device="cuda")
+    return packed, s, torch.where(torch.rand(s.shape, device="cuda", generator=g) < 0.3, ends[(z % 8).long()], z)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", TYPES, ids=name)
+def test_zeros_of_any_byte(k3g, xt, group):
+    """Zeros from 0 to 255, the codes' whole range and beyond it, rows of one group and of more: whole numbers, exact."""
+    for n in (group, 384, 640):
+        for form, aligned, E, T, rows in forms(xt, n):
+            g = gen(T + rows + group)
+            w = any_zeros(g, (E, rows) if E else (rows,), n, group)
+            x = torch.randint(-4, 5, (T, n), device="cuda", generator=g).to(xt)
+            off, expert = even(E, T) if E else (None, None)
+            y = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+            assert bool((y.double() == expect(x, w, E, T, expert)[0]).all()), (form, E, n)
+
+
+@pytest.mark.parametrize("xt", TYPES, ids=name)
+def test_zeros_of_any_byte_in_gated_products(k3g, xt):
+    """w1 with such zeros and w3 without any, and the other way round: both sums are exact, so h is off by the gate's
+    functions alone (16 steps taken, and h's own rounding)."""
+    n, group = 448, 64
+    for form, aligned, E, R, rows in [f for f in forms(xt, n) if f[2]]:
+        g = gen(R + rows)
+        one, two = any_zeros(g, (E, rows), n, group), ref.random_weights(g, (E, rows), n, group, B16, False, exact=True)
+        for w in (one, two):
+            w[1].mul_(2.0 ** -10)
+        x = rows_at(torch.randint(-4, 5, (R, n), device="cuda", generator=g).to(xt), aligned)
+        off, expert = even(E, R)
+        for w1, w3 in ((one, two), (two, one)):
+            assert k3g.k3g_probe_int4_form(xt, R, rows, n, E, True, aligned=aligned) == form
+            h = k3g.k3g_int4_grouped_glu(torch.empty(R, rows, device="cuda"), x, k3g.int4(*w1), k3g.int4(*w3), off)
+            gate, up = [expect(x, w, E, R, expert)[0] for w in (w1, w3)]
+            want = 4 * torch.tanh(gate / 4) / (1 + torch.exp(-gate)) * 25 * torch.tanh(up / 25)
+            assert bool(((h.double() - want).abs() <= 17 * 2.0 ** -24 * want.abs() + 2.0 ** -149).all()), form
