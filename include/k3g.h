@@ -565,11 +565,15 @@ typedef struct {
 /* y[t][r] = sum over groups of scale_rg * sum_{c in g} (n_rc - zero_rg) x_tc for x
  * [T][in] of x_type (x_stride entries between rows) and a single matrix w: the codes
  * go to the matrix cores as they are, no weight is rounded. fp32 x goes in as three
- * bf16 parts whose sum it is. Products are exact, sums fp32 (off by a few 2^-24 of
- * sum scale * (n + zero) * |x|; a group's sum is formed before its scale, and is
- * infinite or NaN where (n + zero) * |x| add up past fp32), y rounded once to y_type.
- * An infinity or NaN in x makes all of its token's outputs infinite or NaN. y rows y_stride entries apart;
- * y must overlap no input. At most 2^30 tokens. */
+ * bf16 parts, whose sum it is in whole steps of 2^-133: entries from 2^-110 on are
+ * taken whole, a smaller one may lose less than a step (a single token's lose
+ * nothing). Products are exact, sums fp32, of n x and of x alone: y is off by a few
+ * 2^-24 of sum |scale| * (n + zero) * |x|, also where codes equal their zero, and of
+ * fp32 x by less than 2^-133 of sum |scale * (n - zero)| besides. A group's sum is
+ * formed before its scale, and is infinite or NaN where (n + zero) * |x| add up past
+ * fp32. y is rounded once to y_type. An infinity or NaN in x makes all of its token's
+ * outputs infinite or NaN. y rows y_stride entries apart; y must overlap no input. At
+ * most 2^30 tokens. */
 int k3g_int4_matmul(void *y, int y_type, int64_t y_stride, const void *x, int x_type, int64_t x_stride, int n_tokens,
                     const k3g_int4 *w, void *stream);
 

@@ -6,9 +6,11 @@
 // exact in bf16 and fp16, and s is applied to the group's sum in fp32, so no
 // weight is ever rounded:
 //   y[t][r] = sum_g s_rg (sum_{c in g} n_rc x_tc - z_rg sum_{c in g} x_tc).
-// The sum of x is a product with ones; -z times it is what the product with the
-// codes starts from, so the two large numbers cancel inside the accumulation and
-// not in two rounded sums.
+// The sum of x is a product with ones; -z times it, rounded, is what the product with
+// the codes starts from, one group (32 columns at least) at a time. The vector kernel forms
+// both sums and subtracts. Either way the result is off by roundings of the two
+// sums, a few 2^-24 of (n + z) |x|: a row whose codes equal their zero gives nearly 0. (The
+// tiles subtract z from the codes, which is exact, and give 0.)
 #pragma once
 
 #include "mxmm.h"
@@ -67,8 +69,9 @@ struct Raw4<K3G_F32> {
     __device__ inline void load(const void *p) { __builtin_memcpy(f, p, 32); }
 };
 
-// And as operand A. fp32 goes in as three bf16 parts whose sum it is: each the
-// leading 8 bits of what the ones before leave.
+// And as operand A. fp32 goes in as three bf16 parts, each the leading 8 bits of what the
+// ones before leave. Their sum is the entry as far down as bf16 goes, 2^-133: from 2^-110 on
+// all 24 bits, of smaller ones all but what is below that step.
 template <int XT>
 struct Act4;
 template <>

@@ -1,4 +1,5 @@
-"""Every kernel of the int4 products, by sizes that each asserts to select it: zeros of any byte."""
+"""Every kernel of the int4 products, by sizes that each asserts to select it: zeros of any byte, fp32's
+smallest entries."""
 import pytest
 import torch
 
@@ -116,3 +117,30 @@ def test_zeros_of_any_byte_in_gated_products(k3g, xt):
             gate, up = [expect(x, w, E, R, expert)[0] for w in (w1, w3)]
             want = 4 * torch.tanh(gate / 4) / (1 + torch.exp(-gate)) * 25 * torch.tanh(up / 25)
             assert bool(((h.double() - want).abs() <= 17 * 2.0 ** -24 * want.abs() + 2.0 ** -149).all()), form
+
+
+def test_fp32_entries_down_to_the_smallest(k3g):
+    """fp32 from its smallest step to 2^-110: the vector kernel takes them whole; the matrix cores' three bf16 parts
+    end at 2^-133, so an entry loses less than that."""
+    n, group = 256, 32
+    for form, aligned, E, T, rows in forms(F32, n):
+        g = gen(T + rows)
+        w = ref.random_weights(g, (E, rows) if E else (rows,), n, group, F32, True)
+        w[1].mul_(2.0 ** 20)
+        e = torch.randint(-149, -109, (T, n), device="cuda", generator=g).double()
+        x = (torch.randn(T, n, device="cuda", generator=g).double() * torch.exp2(e)).float()
+        off, expert = even(E, T) if E else (None, None)
+        y = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+        want, mag = expect(x, w, E, T, expert)
+        lost = torch.zeros_like(want)
+        if form != (8, 1):
+            sums = ref.values(*w)[0].abs().sum(-1)  # of |scale * (code - zero)|
+            lost += 2.0 ** -133 * (sums[expert] if E else sums)
+        steps = ref.roundings(n, group)
+        # products of codes and sums are multiples of 2^-149 as x is; once scaled they lose half of it an addition:
+        # one a group, 8 wavefronts, the output
+        tol = steps * 2.0 ** -24 * mag + lost + (n // group + 9) * 2.0 ** -150
+        err = (y.double() - want).abs()
+        assert bool((err <= tol).all()), (form, E, float((err / tol).max()))
+        y3 = product(k3g, form, aligned, E, T, rows, n, x * 2.0 ** 40, *w, off=off)
+        ref.check(y3, want * 2.0 ** 40, mag * 2.0 ** 40, steps)
