@@ -1,5 +1,5 @@
 """Every kernel of the int4 products, by sizes that each asserts to select it: zeros of any byte, fp32's
-smallest entries."""
+smallest entries, codes that equal their zero, infinities, offsets and sources out of range."""
 import pytest
 import torch
 
@@ -144,3 +144,74 @@ def test_fp32_entries_down_to_the_smallest(k3g):
         assert bool((err <= tol).all()), (form, E, float((err / tol).max()))
         y3 = product(k3g, form, aligned, E, T, rows, n, x * 2.0 ** 40, *w, off=off)
         ref.check(y3, want * 2.0 ** 40, mag * 2.0 ** 40, steps)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", TYPES, ids=name)
+def test_weights_of_value_zero_and_large_entries(k3g, xt, group):
+    """Rows whose codes all equal their zero, between ordinary ones, and entries of any size: what is left is within
+    the sums' roundings of scale * (code + zero) * |x|."""
+    n = 1152
+    for form, aligned, E, T, rows in forms(xt, n):
+        g = gen(T + rows)
+        w = ref.random_weights(g, (E, rows) if E else (rows,), n, group, F32, True)
+        z = w[2].repeat_interleave(group, -1)
+        w[0][..., ::3, :] = (z[..., 0::2] | z[..., 1::2] << 4)[..., ::3, :]
+        x = torch.randn(T, n, device="cuda", generator=g)
+        x = torch.where(torch.rand(T, n, device="cuda", generator=g) < 0.01, 1000 * x, x).to(xt)
+        off, expert = even(E, T) if E else (None, None)
+        y = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+        want, mag = expect(x, w, E, T, expert)
+        assert bool((want[:, ::3] == 0).all())
+        ref.check(y, want, mag, ref.roundings(n, group))
+
+
+@pytest.mark.parametrize("xt", TYPES, ids=name)
+def test_not_finite(k3g, xt):
+    """A token with an infinity or a NaN has no finite output, the tokens beside it keep theirs; likewise a scale."""
+    n = 384
+    for form, aligned, E, T, rows in forms(xt, n):
+        g = gen(T)
+        w = ref.random_weights(g, (E, rows) if E else (rows,), n, 32, F32, True)
+        x = torch.randn(T, n, device="cuda", generator=g).to(xt)
+        off, expert = even(E, T) if E else (None, None)
+        good = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+        bad = sorted({T // 4, T // 2, T - 1})
+        for t, c, v in zip(bad, (7, 380, 100), (float("inf"), float("nan"), -float("inf"))):
+            x[t, c] = v
+        hit = torch.zeros(T, dtype=torch.bool, device="cuda")
+        hit[bad] = True
+        y = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+        assert not torch.isfinite(y[hit]).any() and torch.equal(y[~hit], good[~hit]), (form, E)
+        w[1][..., 11, 4], w[1][..., rows - 1, 0] = float("nan"), float("inf")
+        y = product(k3g, form, aligned, E, T, rows, n, x, *w, off=off)
+        keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+        keep[[11, rows - 1]] = False
+        assert torch.equal(y[~hit][:, keep], good[~hit][:, keep]) and not torch.isfinite(y[:, ~keep]).any(), (form, E)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("xt", TYPES, ids=name)
+def test_groups_and_sources_out_of_range(k3g, xt, glu):
+    """Offsets outside the rows and a perm outside x's: clipped, in every kernel. Rows in no group stay as they were, and so
+    does what lies around y."""
+    n = 160
+    for form, aligned, E, R, rows in [f for f in forms(xt, n) if f[2]]:
+        g = gen(R)
+        w = [k3g.int4(*ref.random_weights(g, (E, rows), n, 32, B16, True)) for _ in range(2)]
+        x = rows_at(torch.randn(R, n, device="cuda", generator=g).to(xt), aligned)
+        perm = torch.full((R,), 2**31 - 1, dtype=torch.int32, device="cuda")
+        perm[::2], perm[1::4] = -5, -2**31
+        inner = torch.sort(torch.randint(-R, 3 * R, (E - 1,), device="cuda", generator=g)).values
+        for lo, hi in ((-7, R + 90), (0, 2**31 - 1), (-2**31, 3 * R), (R, R), (R + 9, R + 9), (5, R - 3)):
+            off = torch.cat([torch.tensor([lo], device="cuda"), inner.clamp(lo, hi), torch.tensor([hi], device="cuda")]).int()
+            assert k3g.k3g_probe_int4_form(xt, R, rows, n, E, glu, aligned=aligned) == form
+            b = torch.full((R + 2, rows + 1), 7.0, device="cuda")
+            y = b[1:R + 1, :rows]
+            for p in (perm, None):
+                if glu:
+                    k3g.k3g_int4_grouped_glu(y, x, *w, off, perm=p, top_k=1)
+                else:
+                    k3g.k3g_int4_grouped_matmul(y, x, w[0], off, perm=p, top_k=1)
+                assert bool((b[[0, -1]] == 7).all() and (b[:, -1] == 7).all()), form
+                assert bool((y[:max(lo, 0)] == 7).all() and (y[max(min(hi, R), 0):] == 7).all()), form
