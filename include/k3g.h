@@ -700,9 +700,13 @@ int k3g_probe_mx_form(int a_format, int kind, int n_rows, int rows, int n_expert
 
 /* k3g_probe_int4_form: the same for int4 products of x_type activations (aligned: x and
  * its row stride on 16-byte addresses): weight rows << 16 | tokens of the tile, for
- * kind 0 k3g_int4_matmul, 1 k3g_int4_grouped_matmul, 2 k3g_int4_grouped_glu. One token: the
- * vector kernel's; up to 64 weight rows: the streaming kernels'. */
+ * kind 0 k3g_int4_matmul, 1 k3g_int4_grouped_matmul, 2 k3g_int4_grouped_glu. 8 by 1: the
+ * vector kernel (one token, two of fp32, rows of experts few of which have two); up to 64
+ * weight rows: the streaming kernels'.
+ * k3g_probe_int4_launch: its launch, workgroups << 4 | wavefronts of each (a streaming
+ * kernel's 4096 of one take an item to themselves). */
 int k3g_probe_int4_form(int x_type, int aligned, int kind, int n_rows, int rows, int in, int n_experts);
+int k3g_probe_int4_launch(int x_type, int aligned, int kind, int n_rows, int rows, int in, int n_experts, int group);
 
 #ifdef __cplusplus
 }

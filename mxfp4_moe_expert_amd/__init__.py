@@ -158,6 +158,7 @@ def lib():
         L.k3g_probe_handoff.argtypes = [i, i, P, P, P]
         L.k3g_probe_mx_form.argtypes = [i, i, i, i, i]
         L.k3g_probe_int4_form.argtypes = [i, i, i, i, i, i, i]
+        L.k3g_probe_int4_launch.argtypes = [i, i, i, i, i, i, i, i]
         _lib = L
     return _lib
 
@@ -934,13 +935,25 @@ def k3g_probe_mx_form(a_format: int, n_rows: int, rows: int, n_experts: int = 0,
 
 def k3g_probe_int4_form(x_type: torch.dtype, n_rows: int, rows: int, n_in: int, n_experts: int = 0, glu: bool = False,
                         aligned: bool = True) -> tuple[int, int]:
-    """(weight rows, tokens) of the tile that an int4 product of these sizes runs on: dense, or of experts. One token:
-    the vector kernel; up to 64 weight rows: the streaming kernels."""
+    """(weight rows, tokens) of the tile that an int4 product of these sizes runs on: dense, or of experts. (8, 1): the
+    vector kernel (one token, two of fp32, rows of experts few of which have two); up to 64 weight rows: the streaming
+    kernels."""
     f = lib().k3g_probe_int4_form(_TYPES[x_type], int(aligned), 2 if glu else 1 if n_experts else 0, n_rows, rows, n_in,
                                   n_experts)
     if f < 0:
         _check("k3g_probe_int4_form", f)
     return f >> 16, f & 0xFFFF
+
+
+def k3g_probe_int4_launch(x_type: torch.dtype, n_rows: int, rows: int, n_in: int, group: int, n_experts: int = 0,
+                          glu: bool = False, aligned: bool = True) -> tuple[int, int]:
+    """(workgroups, wavefronts of each) of that product's launch. Streaming kernels' 4096 workgroups of one wavefront
+    take an item to themselves."""
+    f = lib().k3g_probe_int4_launch(_TYPES[x_type], int(aligned), 2 if glu else 1 if n_experts else 0, n_rows, rows, n_in,
+                                    n_experts, group)
+    if f < 0:
+        _check("k3g_probe_int4_launch", f)
+    return f >> 4, f & 15
 
 
 def pack_bank(experts, n_experts: int, latent: int, inter: int, device="cuda", threads: int = 16):

@@ -227,6 +227,42 @@ __device__ inline void transpose4(uint32_t *v) {
     v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
 }
 
+// A product's items at most (workgroups find the groups' real ones): tiles of `tok` rows by `out` outputs.
+inline int64_t int4_items(const I4Args &a, int mode, int out, int tok) {
+    const int64_t tiles = mode == DENSE ? ((int64_t)a.T + tok - 1) / tok : (int64_t)a.T / tok + (a.E < a.T ? a.E : a.T);
+    return ((int64_t)a.rows + out - 1) / out * tiles;
+}
+
+// A launch: workgroups, and wavefronts of each.
+struct Int4Grid {
+    int64_t workgroups;
+    int waves;
+};
+
+// The vector kernel's: a workgroup takes the outputs of `turns` turns of its wavefronts of one row of y.
+constexpr int kGvWaves = 8;     // wavefronts of a workgroup: wk along a row times those along the outputs
+constexpr int kGvCols = 2048;   // columns of a wavefront's load
+constexpr int kGvGroups = 512;  // workgroups that run at once: two a CU
+constexpr int kGvTurns = 16;    // most turns of four weight rows of a wavefront: a lane keeps one result
+struct GvGrid : Int4Grid {
+    int loads, wk, turns;  // loads of a wavefront, wavefronts along a row
+    int64_t blocks;        // workgroups along the outputs
+};
+inline GvGrid gemv_grid(const I4Args &a, int mode) {
+    GvGrid g;
+    const int all = (a.in + kGvCols - 1) / kGvCols, b = mode == GLU ? 2 : 4;
+    g.loads = all > kGvWaves ? 2 : 1;
+    g.wk = (all + g.loads - 1) / g.loads;
+    const int wr = kGvWaves / g.wk;
+    g.waves = wr * g.wk;
+    const int64_t turns = ((int64_t)a.rows + wr * b - 1) / (wr * b);  // of a workgroup that did all of a row's outputs
+    const int64_t each = (turns * a.T + kGvGroups - 1) / kGvGroups;
+    g.turns = (int)(each < 1 ? 1 : each > kGvTurns ? kGvTurns : each);
+    g.blocks = (turns + g.turns - 1) / g.turns;
+    g.workgroups = g.blocks * a.T;
+    return g;
+}
+
 // A product's launch: int4_gemv.hip, int4_stream_{f32,bf16,f16}.hip, int4_tile_{f32,bf16,f16}.hip
 constexpr int kGvMaxIn = 32768;
 int launch_int4_gemv(const I4Args &a, int mode, int x_type, int group, hipStream_t st);

@@ -1,6 +1,7 @@
 // int4.hip -- products with int4 weights: the calls, their checks, and which
 // kernels they run on.
-#include "int4.h"
+#include "int4_stream.h"
+#include "int4_tile.h"
 
 using namespace k3g;
 
@@ -50,9 +51,11 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 // 38, 512 91, 71; 3584 -> 7168, 64 tokens (224) 20, 29, 128 36, 29 (fp32 49, 55; 512 tokens 162, 206).
 int product_form(const I4Args &a, int mode, int x_type) {
     const bool f32 = x_type == K3G_F32;
-    const bool spread = a.T <= 256 && (f32 ? a.T : 2 * a.T) <= a.E &&
-                        (int64_t)a.rows * a.T <= kMaxRows;  // (its grid is of fewer than 2^32 threads)
-    if (a.in <= kGvMaxIn && (a.T == 1 || (mode == DENSE ? f32 && a.T == 2 : spread))) return form(8, 1);
+    const bool spread = a.T <= 256 && (f32 ? a.T : 2 * a.T) <= a.E && (int64_t)a.rows * a.T <= kMaxRows;
+    if (a.in <= kGvMaxIn && (a.T == 1 || (mode == DENSE ? f32 && a.T == 2 : spread))) {
+        const GvGrid g = gemv_grid(a, mode);
+        if (g.workgroups * g.waves * kWave < (int64_t)1 << 32) return form(8, 1);  // (a launch's limit)
+    }
     const bool wide = !f32 && a.x_vec;
     const int64_t n = mode == DENSE ? a.T : ((int64_t)a.T + a.E - 1) / a.E, most = wide ? 128 : 64;
     const int64_t tiles = mode == DENSE ? (n + most - 1) / most : (n + most - 1) / most * (a.E < a.T ? a.E : a.T);
@@ -160,6 +163,16 @@ int k3g_probe_int4_form(int x_type, int aligned, int kind, int n_rows, int rows,
     I4Args a = {};
     a.T = n_rows, a.rows = rows, a.in = in, a.E = n_experts, a.x_vec = aligned != 0;
     return product_form(a, kind, x_type);
+}
+
+int k3g_probe_int4_launch(int x_type, int aligned, int kind, int n_rows, int rows, int in, int n_experts, int group) {
+    const int f = k3g_probe_int4_form(x_type, aligned, kind, n_rows, rows, in, n_experts);
+    if (f < 0) return f;
+    if ((group != 32 && group != 64 && group != 128) || in % group) return K3G_EINVAL;
+    I4Args a = {};
+    a.T = n_rows, a.rows = rows, a.in = in, a.E = n_experts;
+    const Int4Grid g = f == form(8, 1) ? gemv_grid(a, kind) : f >> 16 <= 64 ? stream_grid(a, kind, group, f) : tile_grid(a, kind, f);
+    return (int)(g.workgroups << 4) | g.waves;
 }
 
 }  // extern "C"

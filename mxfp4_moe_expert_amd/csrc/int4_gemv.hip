@@ -14,11 +14,6 @@
 
 namespace k3g {
 
-constexpr int kGvWaves = 8;    // wavefronts of a workgroup: wk along a row times those along the outputs
-constexpr int kGvCols = 2048;  // columns of a wavefront's load
-constexpr int kGvGroups = 512; // workgroups that run at once: two a CU
-constexpr int kGvTurns = 16;   // most turns of four weight rows of a wavefront: a lane keeps one result
-
 struct GvArgs {
     I4Args a;
     int wk;      // wavefronts along a row
@@ -183,16 +178,12 @@ int launch_int4_gemv(const I4Args &a, int mode, int x_type, int group, hipStream
     g.a = a;
     g.x_type = x_type;
     g.shift = group == 32 ? 0 : group == 64 ? 1 : 2;
-    const int loads = (a.in + kGvCols - 1) / kGvCols, ch = loads > kGvWaves ? 2 : 1, b = mode == GLU ? 2 : 4;
-    g.wk = (loads + ch - 1) / ch;
-    const int wr = kGvWaves / g.wk, waves = wr * g.wk;
-    const int64_t turns = ((int64_t)a.rows + wr * b - 1) / (wr * b);  // of a workgroup that did all of a row's outputs
-    const int64_t each = (turns * a.T + kGvGroups - 1) / kGvGroups;
-    g.turns = (int)(each < 1 ? 1 : each > kGvTurns ? kGvTurns : each);
-    g.blocks = (int)((turns + g.turns - 1) / g.turns);
+    const GvGrid q = gemv_grid(a, mode);
+    const int ch = q.loads, waves = q.waves;
+    g.wk = q.wk, g.turns = q.turns, g.blocks = (int)q.blocks;
     const size_t lds = sizeof(float) * (size_t)g.wk * ch * kGvCols;
     const bool s32 = a.s_type == K3G_F32;
-    const unsigned grid = (unsigned)((int64_t)g.blocks * a.T);
+    const unsigned grid = (unsigned)q.workgroups;
 #define K3G_GV(NW, CH, S32)                                                                                            \
     do {                                                                                                               \
         const void *f = (const void *)int4_gemv_kernel<NW, CH, S32>;                                                   \

@@ -181,22 +181,25 @@ __global__ __launch_bounds__(kI4Waves * kWave, i4_stream_occupancy(RT * (MODE ==
     }
 }
 
+// The launch of a tile (weight rows << 16 | tokens).
+inline Int4Grid stream_grid(const I4Args &a, int mode, int group, int f) {
+    const int units = 4 * i4_stream_steps((f >> 16) / 16, group), turns = (a.in / 32 + units - 1) / units;
+    const int64_t items = int4_items(a, mode, (f >> 16) / (mode == GLU ? 2 : 1), f & 0xFFFF);
+    const bool alone = items >= 4096;
+    const int64_t most = alone ? 4096 : 1024;
+    return {items < most ? (items + 7) / 8 * 8 : most, alone ? 1 : turns < kI4Waves ? turns : kI4Waves};
+}
+
 template <int XT, int GROUP, int MODE, int RT, int NT>
 int launch_int4_stream(const I4Args &a, hipStream_t st) {
     constexpr int TILES = RT * (MODE == GLU ? 2 : 1);
-    constexpr int UNITS = 4 * i4_stream_steps(TILES, GROUP);
-    const int turns = (a.in / 32 + UNITS - 1) / UNITS;
-    const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + 16 * NT - 1) / (16 * NT)
-                                        : (int64_t)a.T / (16 * NT) + (a.E < a.T ? a.E : a.T);
-    const int64_t items = ((int64_t)a.rows + 16 * RT - 1) / (16 * RT) * tiles;
-    const bool alone = items >= 4096;
-    const int waves = alone ? 1 : turns < kI4Waves ? turns : kI4Waves;
-    const int64_t most = alone ? 4096 : 1024, grid = items < most ? (items + 7) / 8 * 8 : most;
+    const Int4Grid g = stream_grid(a, MODE, GROUP, form(16 * TILES, 16 * NT));
+    const int waves = g.waves;
     size_t lds = (size_t)waves * TILES * NT * kWave * 16 + (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
     const void *f = (const void *)int4_stream_kernel<XT, GROUP, MODE, RT, NT>;
     if (lds > 65536 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return K3G_EHIP;
-    int4_stream_kernel<XT, GROUP, MODE, RT, NT><<<(unsigned)grid, waves * kWave, lds, st>>>(a);
+    int4_stream_kernel<XT, GROUP, MODE, RT, NT><<<(unsigned)g.workgroups, waves * kWave, lds, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 

@@ -293,18 +293,22 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
     }
 }
 
+// The launch of a tile (weight rows << 16 | tokens).
+inline Int4Grid tile_grid(const I4Args &a, int mode, int f) {
+    const int64_t items = int4_items(a, mode, (f >> 16) / (mode == GLU ? 2 : 1), f & 0xFFFF), most = 512;
+    return {items < most ? (items + 7) / 8 * 8 : most, 4};
+}
+
 template <int XT, int GROUP, int MODE, int NJ, bool DMA>
 int launch_int4_tile(const I4Args &a, hipStream_t st) {
-    constexpr int OUT = MODE == GLU ? 128 : 256, TOK = 16 * NJ;
-    const int64_t tiles = MODE == DENSE ? ((int64_t)a.T + TOK - 1) / TOK : (int64_t)a.T / TOK + (a.E < a.T ? a.E : a.T);
-    const int64_t items = ((int64_t)a.rows + OUT - 1) / OUT * tiles;
-    const int64_t most = 512, grid = items < most ? (items + 7) / 8 * 8 : most;
+    constexpr int TOK = 16 * NJ;
+    const Int4Grid g = tile_grid(a, MODE, form(256, TOK));
     const size_t lds = 2 * (size_t)i4_step_bytes<XT, NJ>() + i4_scale_bytes<GROUP>() + 8 * TOK +
                        (MODE == DENSE ? 0 : 4 * ((size_t)a.E + 1 + 16));
     const void *f = (const void *)int4_tile_kernel<XT, GROUP, MODE, NJ, DMA>;
     if (lds > 65536 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return K3G_EHIP;
-    int4_tile_kernel<XT, GROUP, MODE, NJ, DMA><<<(unsigned)grid, 256, lds, st>>>(a);
+    int4_tile_kernel<XT, GROUP, MODE, NJ, DMA><<<(unsigned)g.workgroups, 256, lds, st>>>(a);
     return hipGetLastError() == hipSuccess ? K3G_OK : K3G_EHIP;
 }
 
