@@ -29,26 +29,36 @@ int use_int4(I4Args *a, int slot, const k3g_int4 *w, Span *covers) {
 
 // The kernel of a product: weight rows << 16 | tokens of its tile; the vector kernel's is 8 << 16 | 1.
 //
-// A single row runs on the vector units, and so do two of fp32, and rows of experts, a workgroup's row each, where
-// few experts would have two (us; vector, streamed): one bf16 token 7168 -> 3584 8.6, 9.4; two 9.7, 9.5, fp32 9.8, 16, three
-// 15, 16. Of 256 experts of 3584 x 3584, groups of 32, 64 rows 91, 132, 128 rows 149, 215, 256 286, 307 (groups of 128 145, 173
-// by 128, 213, 205 by 192); fp32 128 rows 150, 351, 256 279, 483. More than 256 rows are streamed: rows that crowd
-// on one expert cost this kernel what rows of many do.
+// Figures are us, of groups of 64 with zeros and fp32 in brackets where nothing else is said; "experts" are 256 of
+// 3584 x 3584 whose rows are spread evenly, by their average rows. Every border was measured on all three groups.
 //
-// Tiles of 256 outputs pay where rows are many and items enough to fill half of the chip (streamed, tiled): bf16 3584
-// -> 7168, 512 tokens (112 items) 100, 100, 1024 tokens (224) 182, 102; 7168 -> 3584, 1024 tokens (112) 138, 185, 1536
-// (168) 207, 184.
-// fp32 (64 tokens a tile) 7168 -> 3584, 512 tokens (112) 144, 219, 1024 (224) 253, 222. Grouped, by the average rows of the
-// bank's experts: 256 of 3584 x 3584, bf16, 16 rows 584, 623, 32 rows 873, 698; fp32 64 rows 635, 684, 128 rows 1133, 1025.
+// A single row runs on the vector units, and so do two of fp32, and rows of experts, a workgroup's row each, where
+// few experts would have two (vector, streamed). One token 7168 -> 3584 9.9, 9.4 (9.9, 16; groups of 32 10.3,
+// 11.1), two 12, 9.6 (12, 16), three 16, 9.7 (16.2, 16.6). Experts, 64 rows in all 106, 110 (106, 191), 128 182,
+// 182 (182, 322), 192 266, 221, 256 337, 257 (337, 461); groups of 32 128 rows 186, 257, of 128 180, 173; one
+// token's 16 of 3584 x 3072, gated, 40, 60. It reads a matrix once a row, so it loses where rows crowd: on a
+// routing that prefers some experts (the 16 best of scores some of which are higher) 64 rows 103, 99, 128 180, 163
+// (179, 280), 256 rows of 896 experts of 3584 x 3072 296, 251; 128 rows on 8 experts 143, 34, 256 on 8 (268, 73).
+// More than 256 rows are streamed.
+//
+// Tiles of 256 outputs pay where rows are many and items enough to fill half of the chip (streamed, tiled; items
+// of 128 tokens, fp32 64). 3584 -> 7168, 512 tokens (112 items) 91, 95, 1024 (224) 151, 95; 7168 -> 3584, 1024
+// (112) 149, 180, 1536 (168) 213, 181; groups of 32 1536 tokens 240, 222, 2048 278, 222. fp32 512 tokens (112)
+// 156, 218, 1024 (224) 262, 222. Rows off 16-byte addresses take fp32's tile and border: 1024 tokens 137, 170,
+// 2048 222, 226, 4096 436, 447, so their tile, whose staged rows lie in scratch memory, does not pay yet. Experts:
+// 16 rows 611, 654, 20 667, 661, 32 914, 696; fp32 32 rows 1524, 1456, 48 2071, 1720, 64 2499, 2438, 80 3118,
+// 3232, 96 3653, 3214, 128 4673, 3991 (groups of 48 rows take one tile of 64, of 80 two: the border leaves 48 rows
+// a sixth slower than they could be).
 //
 // Streamed, 64 outputs by 32 tokens, or 32 by 16 where half a tile would be empty or where those are at most two
-// workgroups a CU, which run at once (32 x 16 first; bf16, fp32 in brackets): 7168 -> 3584, 64 tokens (448) 23, 31 (34, 40),
-// 80 (560) 33, 28 (50, 37); 3584 -> 7168, 32 (448) 15, 20 (21, 26), 33 (672) 20, 18 (27, 25); 4096 -> 1024, 128 (256) 9.7, 17
-// (14, 25); 3584 -> 14336, 16 (448) 15, 18 (21, 21), 17 23, 20 (36, 26). Grouped, 256 of 3584 x 3584, 9 rows 575, 650 (896,
-// 799), 11 rows 591, 659, 14 rows 694, 696; fp32 8 rows 837, 890. Up to 16 tokens of few outputs take 16 a workgroup: 7168 ->
-// 3584, 16 tokens 13, 16; 3584 -> 7168 12, 11. Where
-// 64 x 32 would be more than a workgroup a CU, bf16 and fp16 take 64 x 64: 7168 -> 3584, 128 tokens (224) 25, 39, 192 47,
-// 38, 512 91, 71; 3584 -> 7168, 64 tokens (224) 20, 29, 128 36, 29 (fp32 49, 55; 512 tokens 162, 206).
+// workgroups a CU, which run at once (32 x 16 first): 7168 -> 3584, 64 tokens (448 workgroups) 22, 27 (36, 40), 80
+// (560) 30, 25 (50, 37); 3584 -> 7168, 32 (448) 14, 17 (21, 26), 33 (672) 17, 16 (26, 25); 4096 -> 1024, 128 (256)
+// 8.7, 16 (13, 24); 3584 -> 14336, 16 (448) 15, 16 (22, 21), 17 23, 18 (36, 26). Experts: 12 rows 541, 585, 13
+// 577, 588, 14 612, 596; fp32 6 rows 813, 753, 8 826, 780, groups of 128 8 rows 813, 850, 12 863, 913. Up to 16
+// tokens of few outputs take 16 a workgroup (16 x 16, 32 x 16): 7168 -> 3584 12, 15 (19, 23); 3584 -> 7168 11.4,
+// 9.9 (18, 14). Where 64 x 32 would be more than a workgroup a CU, bf16 and fp16 take 64 x 64 (64 x 32 first):
+// 7168 -> 3584, 128 tokens (224) 27, 40, 192 (336) 48, 39, 512 93, 74; 3584 -> 7168, 64 tokens (224) 17, 26, 128
+// (448) 30, 25.
 int product_form(const I4Args &a, int mode, int x_type) {
     const bool f32 = x_type == K3G_F32;
     const bool spread = a.T <= 256 && (f32 ? a.T : 2 * a.T) <= a.E && (int64_t)a.rows * a.T <= kMaxRows;

@@ -6,10 +6,16 @@
 //
 // A step of 128 columns is 128 matrix and about 650 vector instructions a wavefront
 // at groups of 64: 304 make operands of 8192 codes, 256 apply the groups' scales to
-// the partial sums. Issue bounds it: 4096 tokens 7168 -> 6144 393-410 us, 0.88-0.92
-// PFLOP/s, matrix cores 31-36% busy; 65536 rows over 536 experts of 3584 x 3072 2.8 ms,
-// their gated up-products 6.1. Two workgroups a CU take each other's waits: one alone
-// needs 0.7 of the time of two.
+// the partial sums. 4096 tokens 7168 -> 6144 386 us, 0.93 PFLOP/s; 65536 rows over 536
+// experts of 3584 x 3072 2.8 ms, their gated up-products 6.1. Matrix cores are busy
+// 36% of that time and the vector units 46%: the two hardly overlap, since the operands of a half
+// step are made before its first product and each two token tiles begin with a branch and a
+// wait for their rows. Two workgroups a CU take each other's waits: one alone needs 0.7 of
+// the time of two.
+//
+// bf16 and fp16 rows off 16-byte addresses come through registers, which the compiler keeps in
+// scratch memory: a step waits for the next one's rows (4096 tokens 7168 -> 3584 447 us; fp32's
+// tile for rows on such addresses 446, the one by DMA 256).
 #pragma once
 
 #include "int4.h"
@@ -112,7 +118,8 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a) {
             for (int t = 0; t < TILES; ++t) w[t] = load16((t < RT ? w0 : w1) + (at[t] + c));
         };
         // The bases are made anew each time (the empty assembly hides them): kept, the lanes' addresses would not fit the
-        // registers, and a reload from scratch memory waits for every load under way.
+        // registers, and a reload from scratch memory waits for every load under way. (Up to 16 registers that are
+        // spilled all the same are loaded again between items, not in the loop over steps.)
         auto load_s = [&](int turn) {
             const int g0 = turn * NG, from = max(min(g0, a.G - NG), 0), size = a.s_type == K3G_F32 ? 4 : 2;
             s_shift = g0 - from;
